@@ -281,6 +281,164 @@ SDPA_API sdpa_status sdpa_forward_planned(const void *q, const void *k, const vo
                                  sdpa_stream_t stream);
 
 /*
+ * Backward pass.
+ *
+ * sdpa_backward: the gradients of one forward call, given the gradient of its
+ * output.  The probabilities are recomputed from the forward call's
+ * log-sum-exp; no [L, S] matrix is stored.
+ *   P = exp(scale Q K^T - lse), 0 where masked;  delta = rowsum(dout out) - dlse
+ *   dS = P (dout V^T - delta);  dq = scale dS K,  dk = scale dS^T Q,  dv = P^T dout
+ * summed over the query heads that share a KV head.
+ *   q, k, v, out   as given to and written by the forward call
+ *   lse            [B][Hq][L] fp32, written by sdpa_forward_ex (options.lse)
+ *   dout           [B][Hq][L][Dv], gradient of out
+ *   dq, dk, dv     gradients, shaped and typed like q, k, v; every element is
+ *                  written (0 for keys that no row sees)
+ *   the rest       as in the forward call; opt may be NULL
+ * A row whose lse is -inf contributes nothing.  The sums run in a fixed order:
+ * the same call gives the same bits.  P and dS are rounded to the 16-bit type
+ * (fp16: after scaling by powers of two, so that small gradients need no loss
+ * scale to survive it); all sums are fp32.
+ * Workspace: sdpa_backward_workspace_bytes(...) bytes, always above 0;
+ * workspace NULL with workspace_bytes 0 takes it stream-ordered from the pool
+ * like sdpa_forward.  Nothing in it needs clearing.
+ * Errors: as sdpa_forward, and SDPA_ERR_INVALID_ARG when a gradient overlaps
+ * an input or another gradient, for a misaligned lse, dlse, sinks or dsinks,
+ * or for dsinks without sinks; SDPA_ERR_RESOURCES when the workspace is too
+ * small.
+ */
+typedef enum {
+  SDPA_BWD_PATH_AUTO = 0,
+  SDPA_BWD_PATH_TILE = 1, /* 64-row tiles on warp-level tensor-core tiles, any
+                             head dims                                      */
+  SDPA_BWD_PATH_TC = 2    /* 128-row tiles on tcgen05 with TMEM accumulators,
+                             head dims up to 256                            */
+} sdpa_backward_path;
+
+/* Options of sdpa_backward (zero-initialise, then set what is needed). */
+typedef struct {
+  int has_q_offset; /* as in sdpa_options */
+  int q_offset;
+  const float *sinks; /* [Hq] sink logits of the forward call                */
+  float *dsinks;      /* [Hq] their gradient (needs sinks)                   */
+  const float *dlse;  /* [B][Hq][L] gradient of lse, where lse was used
+                         (a merge of results over disjoint key ranges)       */
+  int force_path;     /* sdpa_backward_path; 0 = the router's choice         */
+} sdpa_backward_options;
+
+SDPA_API sdpa_status sdpa_backward(const void *q, const void *k, const void *v, const void *out,
+                                   const float *lse, const void *dout, void *dq, void *dk,
+                                   void *dv, int B, int Hq, int Hkv, int L, int S, int Dqk,
+                                   int Dv, float scale, int causal, int window_size,
+                                   sdpa_dtype dtype, const sdpa_backward_options *opt,
+                                   void *workspace, size_t workspace_bytes,
+                                   sdpa_stream_t stream);
+
+/*
+ * Workspace of sdpa_backward for this problem on the current device (of its
+ * options only has_q_offset, q_offset and force_path matter).  Returns 0 and
+ * sets the last error message when the arguments are invalid.
+ */
+SDPA_API size_t sdpa_backward_workspace_bytes(int B, int Hq, int Hkv, int L, int S, int Dqk,
+                                              int Dv, int causal, int window_size,
+                                              sdpa_dtype dtype, const sdpa_backward_options *opt);
+
+/*
+ * Rotary positions (RoPE) and their gradient.
+ *
+ * Pairs (a, b) of a head's first rotary_dim elements turn by the angle
+ * position * frequency of the pair; the other elements are copied:
+ *   (a, b) -> m (a cos t - b sin t, a sin t + b cos t),   t = position * w_i.
+ * interleaved = 0 pairs element i with i + rotary_dim/2, interleaved = 1
+ * pairs 2i with 2i + 1.  The unscaled frequency of pair i is
+ * w_i = base^(-2i / rotary_dim); for positions past the trained length:
+ *   SDPA_ROPE_LINEAR  w_i / factor
+ *   SDPA_ROPE_NTK     base replaced by base * factor^(R / (R - 2)), R = rotary_dim
+ *   SDPA_ROPE_YARN    pairs of many turns over original_length keep w_i, pairs
+ *                     of few take w_i / factor, with a ramp over the pair index
+ *                     between the indices of beta_fast and beta_slow turns
+ *                     (floor and ceiling); m = 0.1 ln(factor) + 1 unless given
+ *   SDPA_ROPE_BANDED  the same with a ramp over the number of turns itself,
+ *                     from beta_slow (all scaled) to beta_fast (all kept)
+ */
+typedef enum {
+  SDPA_ROPE_PLAIN = 0,
+  SDPA_ROPE_LINEAR = 1,
+  SDPA_ROPE_NTK = 2,
+  SDPA_ROPE_YARN = 3,
+  SDPA_ROPE_BANDED = 4
+} sdpa_rope_scaling;
+
+/* What sdpa_rotary_init reads (zero-initialise, then set what is needed). */
+typedef struct {
+  int head_dim;        /* elements of one head, 2 to 512                        */
+  int rotary_dim;      /* rotated elements, even, 2 to head_dim; 0 = head_dim   */
+  int interleaved;     /* 0 halves, 1 neighbours                                */
+  double base;         /* 0 = 10000                                             */
+  int scaling;         /* sdpa_rope_scaling                                     */
+  double factor;       /* > 0 with a scaling: new length over trained length    */
+  int original_length; /* trained length (yarn, banded)                         */
+  double beta_fast;    /* 0 = 32 (yarn) or 4 (banded) turns                     */
+  double beta_slow;    /* 0 = 1 turn                                            */
+  double magnitude;    /* m; 0 = the scaling's own (1, or yarn's)               */
+} sdpa_rotary_config;
+
+/*
+ * A filled plan: plain host memory without pointers, to be kept and copied
+ * freely.  turns[i] is pair i's frequency in turns per position, as a 64-bit
+ * fixed-point fraction of a turn (2^64 = one turn): position * turns modulo
+ * 2^64 is the angle, exact for every 64-bit position, so far positions lose
+ * nothing.
+ */
+typedef struct {
+  int head_dim, rotary_dim, interleaved;
+  float magnitude;
+  uint64_t turns[256];
+} sdpa_rotary_plan;
+
+/* Host-only.  SDPA_ERR_INVALID_ARG names the field that breaks its range. */
+SDPA_API sdpa_status sdpa_rotary_init(const sdpa_rotary_config *config, sdpa_rotary_plan *plan);
+
+/* Element strides of a [B][heads][L][head_dim] view; head_dim is contiguous. */
+typedef struct {
+  long long batch, head, token;
+} sdpa_strides;
+
+typedef struct {
+  const void *x;
+  void *out;
+  int heads;
+  sdpa_strides x_strides, out_strides;
+} sdpa_rotary_tensor;
+
+/*
+ * sdpa_rotary: rotate one or two tensors (commonly q and k) of B sequences of
+ * L tokens in one launch.
+ *   tensors / count  1 or 2 views of 16-bit elements.  Strides are free, so
+ *       that slices of a fused projection [B][L][heads][head_dim] go in and
+ *       the dense [B][heads][L][head_dim] that sdpa_forward takes comes out, or
+ *       the other way round for the gradient.  out may be x itself (same
+ *       strides: in place); otherwise its extent must not meet x's.  Out
+ *       strides must keep all elements apart.  The tensors of one call must not
+ *       write what another of them reads or writes.
+ *   positions  device array of int32 (position_bits = 32) or int64 (64)
+ *       positions, element [b * position_batch_stride + l]; NULL (bits 0):
+ *       token l is at position l.  `offset` is added to every position.
+ *   inverse    0: rotate.  1: the transpose, i.e. the gradient with respect to x
+ *       given the gradient with respect to out (angles negated, same m).
+ * Angles are exact to 2^-32 of a turn, cos, sin and the products are fp32, and
+ * each result is rounded once, to nearest even.
+ * Errors: SDPA_ERR_INVALID_ARG (NULL pointers, sizes below 1, misaligned
+ * pointers, overlap as above, an unfilled plan), SDPA_ERR_UNSUPPORTED (dtype,
+ * more than 2^31 tokens), SDPA_ERR_CUDA.
+ */
+SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan, const sdpa_rotary_tensor *tensors,
+                                 int count, int B, int L, const void *positions,
+                                 int position_bits, long long position_batch_stride,
+                                 long long offset, int inverse, sdpa_dtype dtype,
+                                 sdpa_stream_t stream);
+
+/*
  * Device watchdog.  Every wait inside the kernels (on an mbarrier or a
  * tensor-core completion) gives up after a bounded time, records a code in a
  * device word and lets the kernel exit cleanly instead of hanging.

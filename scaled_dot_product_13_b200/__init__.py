@@ -19,6 +19,8 @@ import ctypes
 import os
 
 __all__ = ["forward", "forward_ws", "forward_noalloc", "forward_ex", "Options", "workspace_bytes", "plan", "device_status",
+           "backward", "backward_workspace_bytes", "BackwardOptions", "BWD_PATH_AUTO", "BWD_PATH_TILE", "BWD_PATH_TC",
+           "rotary", "rotary_plan", "RotaryPlan", "ROPE_SCALINGS",
            "set_wait_limit_ns", "watchdog_selftest", "exp2_selftest", "time_next_main_kernel", "time_next_call", "load_library", "library_path",
            "SdpaError", "PATH_AUTO", "PATH_SPLITKV", "PATH_TC", "PATH_TC2", "PATH_WIDE", "PATH_TC_DUAL", "PATH_TC_KSPLIT",
            "PATH_TC2_LOOP", "STATUS"]
@@ -28,6 +30,7 @@ _LIB: ctypes.CDLL | None = None
 
 PATH_AUTO, PATH_SPLITKV, PATH_TC, PATH_TC2, PATH_WIDE, PATH_TC_DUAL, PATH_TC_KSPLIT, PATH_TC2_LOOP = \
     0, 1, 2, 3, 4, 5, 6, 7
+BWD_PATH_AUTO, BWD_PATH_TILE, BWD_PATH_TC = 0, 1, 2
 STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTED",
           3: "SDPA_ERR_RESOURCES", 4: "SDPA_ERR_CUDA", 5: "SDPA_ERR_TIMEOUT"}
 
@@ -57,6 +60,41 @@ class PlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class BackwardOptions(ctypes.Structure):
+    """Mirror of sdpa_backward_options."""
+    _fields_ = [("has_q_offset", ctypes.c_int), ("q_offset", ctypes.c_int),
+                ("sinks", ctypes.c_void_p), ("dsinks", ctypes.c_void_p), ("dlse", ctypes.c_void_p),
+                ("force_path", ctypes.c_int)]
+
+
+class RotaryConfig(ctypes.Structure):
+    """Mirror of sdpa_rotary_config."""
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("base", ctypes.c_double), ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_int), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class RotaryPlan(ctypes.Structure):
+    """Mirror of sdpa_rotary_plan: host memory only, filled by ``rotary_plan``."""
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("magnitude", ctypes.c_float), ("turns", ctypes.c_uint64 * 256)]
+
+
+class Strides(ctypes.Structure):
+    """Mirror of sdpa_strides."""
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+
+
+class RotaryTensor(ctypes.Structure):
+    """Mirror of sdpa_rotary_tensor."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_strides", Strides), ("out_strides", Strides)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+
+
 def library_path() -> str:
     return os.environ.get("SDPA_LIBRARY", os.path.join(_HERE, "libsdpa.so"))
 
@@ -81,6 +119,13 @@ def load_library() -> ctypes.CDLL:
     lib.sdpa_workspace_bytes.argtypes = [i] * 10
     lib.sdpa_workspace_bytes.restype = sz
     lib.sdpa_plan.argtypes = [i] * 13 + [ctypes.POINTER(PlanInfo)]
+    lib.sdpa_backward.argtypes = [vp] * 9 + [i] * 7 + [f, i, i, i, ctypes.POINTER(BackwardOptions), vp, sz, vp]
+    lib.sdpa_backward_workspace_bytes.argtypes = [i] * 10 + [ctypes.POINTER(BackwardOptions)]
+    lib.sdpa_backward_workspace_bytes.restype = sz
+    ll = ctypes.c_longlong
+    lib.sdpa_rotary_init.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(RotaryPlan)]
+    lib.sdpa_rotary.argtypes = [ctypes.POINTER(RotaryPlan), ctypes.POINTER(RotaryTensor), i, i, i, vp, i, ll, ll,
+                                i, i, vp]
     lib.sdpa_device_status.argtypes = [i]
     lib.sdpa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.sdpa_set_wait_limit_ns.restype = None
@@ -94,7 +139,7 @@ def load_library() -> ctypes.CDLL:
     lib.sdpa_status_string.argtypes = [i]
     lib.sdpa_last_error_message.restype = ctypes.c_char_p
     for fn in ("sdpa_forward", "sdpa_forward_ws", "sdpa_forward_noalloc", "sdpa_forward_ex",
-               "sdpa_forward_planned", "sdpa_plan",
+               "sdpa_forward_planned", "sdpa_plan", "sdpa_rotary_init", "sdpa_rotary", "sdpa_backward",
                "sdpa_device_status", "sdpa_watchdog_selftest", "sdpa_exp2_selftest"):
         getattr(lib, fn).restype = ctypes.c_int
     _LIB = lib
@@ -257,6 +302,165 @@ def plan(B, Hq, Hkv, L, S, Dqk, Dv, causal=False, window_size=0, dtype="bf16",
     _check(lib.sdpa_plan(B, Hq, Hkv, L, S, Dqk, Dv, int(bool(causal)), int(window_size), dt,
                          int(num_sms), int(force_path), int(force_splits), ctypes.byref(info)))
     return info.as_dict()
+
+
+def backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, causal=False, window_size=0, dtype="bf16",
+                             q_offset: int | None = None, force_path: int = 0) -> int:
+    """Workspace that ``backward`` needs for this problem on the current device."""
+    lib = load_library()
+    opt = BackwardOptions()
+    if q_offset is not None:
+        opt.has_q_offset, opt.q_offset = 1, int(q_offset)
+    opt.force_path = int(force_path)
+    n = lib.sdpa_backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, int(bool(causal)), int(window_size),
+                                          0 if dtype in ("bf16", "bfloat16") else 1, ctypes.byref(opt))
+    if n == 0:
+        msg = lib.sdpa_last_error_message().decode(errors="replace")
+        raise SdpaError(1, msg)
+    return n
+
+
+def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool = False, window_size: int = 0,
+             q_offset: int | None = None, sinks=None, dlse=None, dq=None, dk=None, dv=None, dsinks=None,
+             stream=None, workspace=None, force_path: int = 0):
+    """Gradients (dq, dk, dv) of ``forward_ex(q, k, v, ..., lse=lse)``, given its
+    ``out`` and ``lse`` and the gradient ``dout`` of out; the other arguments as
+    in that call.  ``dlse``: gradient [B, Hq, L] (float32) of lse, where it was
+    used.  ``dsinks``: float32 [Hq] that receives the gradient of ``sinks``.
+    ``dq`` / ``dk`` / ``dv``: contiguous tensors to write (new ones when None).
+    ``workspace``: at least ``backward_workspace_bytes`` bytes on the device,
+    not used by other work until the call's kernels are done.  None: from
+    torch's caching allocator on the current stream, or, with ``stream`` given,
+    from the stream-ordered pool."""
+    import torch
+
+    lib = load_library()
+    B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
+    sc = float(Dqk ** -0.5 if scale is None else scale)
+    dt = _dtype_code(q)
+    for name, t in (("k", k), ("v", v)):
+        if t.device != q.device:
+            raise SdpaError(1, f"{name} must be on q's device")
+
+    def want(name, t, shape, dtype):
+        if t is not None and not (t.device == q.device and t.dtype == dtype and t.is_contiguous()
+                                  and tuple(t.shape) == tuple(shape)):
+            raise SdpaError(1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on q's device")
+
+    for name, t in (("out", out), ("lse", lse), ("dout", dout)):
+        if t is None:
+            raise SdpaError(1, f"{name} is needed")
+    want("out", out, (B, Hq, L, Dv), q.dtype)
+    want("dout", dout, (B, Hq, L, Dv), q.dtype)
+    want("dq", dq, q.shape, q.dtype)
+    want("dk", dk, k.shape, q.dtype)
+    want("dv", dv, v.shape, q.dtype)
+    want("lse", lse, (B, Hq, L), torch.float32)
+    want("dlse", dlse, (B, Hq, L), torch.float32)
+    want("sinks", sinks, (Hq,), torch.float32)
+    want("dsinks", dsinks, (Hq,), torch.float32)
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise SdpaError(1, "workspace must be contiguous and on q's device")
+    opt = BackwardOptions()
+    if q_offset is not None:
+        opt.has_q_offset, opt.q_offset = 1, int(q_offset)
+    opt.sinks, opt.dsinks, opt.dlse = (t.data_ptr() if t is not None else None for t in (sinks, dsinks, dlse))
+    opt.force_path = int(force_path)
+    with torch.cuda.device(q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None and stream is None:
+            n = lib.sdpa_backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, int(bool(causal)), int(window_size),
+                                                  dt, ctypes.byref(opt))
+            # invalid problems are left for the call to name
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        ws_ptr = 0 if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.sdpa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                 dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, L, S,
+                                 Dqk, Dv, sc, int(bool(causal)), int(window_size), dt, ctypes.byref(opt), ws_ptr,
+                                 ws_bytes, _call_stream(stream, q.device)))
+    return dq, dk, dv
+
+
+def rotary_plan(head_dim: int, rotary_dim: int | None = None, base: float = 10000.0,
+                interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                original_length: int = 0, beta_fast: float | None = None,
+                beta_slow: float | None = None, magnitude: float | None = None) -> RotaryPlan:
+    """The frequencies of ``rotary``, computed once on the host (no CUDA call).
+    ``scaling``: "none", "linear", "ntk", "yarn" or "banded", with ``factor``
+    and (yarn, banded) ``original_length``; see sdpa_rotary_config."""
+    if scaling not in ROPE_SCALINGS:
+        raise SdpaError(1, f"scaling must be one of {', '.join(ROPE_SCALINGS)} (got {scaling!r})")
+    for name, x in (("rotary_dim", rotary_dim), ("base", base), ("beta_fast", beta_fast),
+                    ("beta_slow", beta_slow), ("magnitude", magnitude)):
+        if x is not None and x == 0:  # 0 means "default" in the C structure
+            raise SdpaError(1, f"{name} must not be 0")
+    cfg = RotaryConfig(int(head_dim), int(rotary_dim or 0), int(bool(interleaved)), float(base),
+                       ROPE_SCALINGS[scaling], float(factor), int(original_length),
+                       float(beta_fast or 0), float(beta_slow or 0), float(magnitude or 0))
+    out = RotaryPlan()
+    _check(load_library().sdpa_rotary_init(ctypes.byref(cfg), ctypes.byref(out)))
+    return out
+
+
+def _call_stream(stream, device):
+    """The handle of ``stream``, by default the current stream of ``device``."""
+    import torch
+
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def rotary(plan: RotaryPlan, q, k=None, positions=None, offset: int = 0, inverse: bool = False,
+           out_q=None, out_k=None, stream=None):
+    """Rotate ``q`` (and ``k``) [B, H, L, head_dim] by their positions; returns
+    the result(s).  Any strides with a contiguous last dim: a projection
+    [B, L, H, D] goes in as ``x.transpose(1, 2)``.  ``positions``: int32 or
+    int64 CUDA tensor [L], [1, L] or [B, L] (default 0..L-1), ``offset`` added.
+    ``inverse=True`` is the gradient.  ``out_q`` / ``out_k``: views to write
+    (the inputs themselves: in place); by default new dense [B, H, L, D]."""
+    import torch
+
+    lib = load_library()
+    if not isinstance(plan, RotaryPlan):
+        raise SdpaError(1, "plan must come from rotary_plan")
+    if k is None and out_k is not None:
+        raise SdpaError(1, "out_k without k")
+    pairs = [("q", q, out_q)] + ([("k", k, out_k)] if k is not None else [])
+    tensors, outs = (RotaryTensor * 2)(), []
+    for name, x, _ in pairs:
+        if x.dim() != 4 or x.shape[3] != plan.head_dim:
+            raise SdpaError(1, f"{name} must be [B, H, L, {plan.head_dim}] (got {tuple(x.shape)})")
+        if not x.is_cuda or x.device != q.device:
+            raise SdpaError(1, f"{name} must be a CUDA tensor, on q's device")
+        if x.dtype != q.dtype or (x.shape[0], x.shape[2]) != (q.shape[0], q.shape[2]):
+            raise SdpaError(1, "q and k must share dtype, batch and length")
+        if x.stride(3) != 1:
+            raise SdpaError(1, f"{name}'s last dim must be contiguous")
+    B, _, L, D = (int(n) for n in q.shape)
+    dt = _dtype_code(q)
+    pos_ptr, bits, pos_stride = None, 0, 0
+    if positions is not None:
+        if positions.device != q.device or positions.dtype not in (torch.int32, torch.int64):
+            raise SdpaError(1, "positions must be an int32 or int64 tensor on q's device")
+        if tuple(positions.shape) not in ((L,), (1, L), (B, L)) or (L > 1 and positions.stride(-1) != 1):
+            raise SdpaError(1, f"positions must be [L], [1, L] or [B, L] with L = {L}, contiguous along L")
+        pos_ptr, bits = positions.data_ptr(), 32 if positions.dtype == torch.int32 else 64
+        if positions.dim() == 2 and positions.shape[0] == B and B > 1:
+            pos_stride = positions.stride(0)
+    with torch.cuda.device(q.device):
+        for n, (name, x, out) in enumerate(pairs):
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or out.stride(3) != 1:
+                raise SdpaError(1, f"out_{name} must have {name}'s shape, dtype and device, its last dim contiguous")
+            tensors[n] = RotaryTensor(x.data_ptr(), out.data_ptr(), x.shape[1], Strides(*x.stride()[:3]),
+                                      Strides(*out.stride()[:3]))
+            outs.append(out)
+        _check(lib.sdpa_rotary(ctypes.byref(plan), tensors, len(pairs), B, L, pos_ptr, bits, pos_stride,
+                               int(offset), int(bool(inverse)), dt, _call_stream(stream, q.device)))
+    return outs[0] if k is None else tuple(outs)
 
 
 def _num_sms() -> int:

@@ -522,12 +522,8 @@ sdpa_status forward_call(const Problem &pb, const void *q, const void *k, const 
   bool allocated = false;
   if (pl.ws_bytes > 0) {
     if (own_ws) {
-      cudaError_t e = g_test_hooks.fail_alloc ? cudaErrorMemoryAllocation
-                                              : cudaMallocAsync(&ws, pl.ws_bytes, stream);
-      if (e != cudaSuccess)
-        return fail(SDPA_ERR_CUDA, "cudaMallocAsync(%zu bytes) for the split workspace: %s%s",
-                    pl.ws_bytes, cudaGetErrorString(e),
-                    g_test_hooks.fail_alloc ? " (injected by SDPA_TEST_FAIL_ALLOC)" : "");
+      st = pool_alloc(&ws, pl.ws_bytes, stream, "split");
+      if (st != SDPA_OK) return st;
       allocated = true;
     } else {
       if (ws == nullptr || ws_bytes < pl.ws_bytes)
@@ -579,6 +575,8 @@ sdpa_status current_context_id(unsigned long long *id) {
   return f.get_id(ctx, id) == CUDA_SUCCESS ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
+sdpa_status validate_problem(const Problem &pb) { return validate_shape(pb); }
+
 sdpa_status validate_call(const Problem &pb, const void *q, const void *k, const void *v,
                           const void *out) {
   sdpa_status st = validate_shape(pb);
@@ -594,6 +592,27 @@ sdpa_status plan_call(const Problem &pb, int force_path, int force_splits, Plan 
   st = device_state(&dev, &sms, &wd);
   if (st != SDPA_OK) return st;
   return make_plan(pb, sms, force_path, force_splits, plan);
+}
+
+sdpa_status device_info(int *sms, unsigned int **wd_word, uint64_t *wait_limit_ns) {
+  int dev;
+  sdpa_status st = device_state(&dev, sms, wd_word);
+  if (st == SDPA_OK) *wait_limit_ns = wait_limit();
+  return st;
+}
+
+sdpa_status pool_alloc(void **ptr, size_t bytes, cudaStream_t stream, const char *what) {
+  cudaError_t e =
+      g_test_hooks.fail_alloc ? cudaErrorMemoryAllocation : cudaMallocAsync(ptr, bytes, stream);
+  if (e != cudaSuccess)
+    return fail(SDPA_ERR_CUDA, "cudaMallocAsync(%zu bytes) for the %s workspace: %s%s", bytes, what,
+                cudaGetErrorString(e),
+                g_test_hooks.fail_alloc ? " (injected by SDPA_TEST_FAIL_ALLOC)" : "");
+  return SDPA_OK;
+}
+
+bool extents_meet(const void *a, size_t na, const void *b, size_t nb) {
+  return overlaps(a, na, b, nb);
 }
 
 sdpa_status set_error(sdpa_status st, const std::string &msg) { return fail_str(st, msg); }

@@ -1,0 +1,213 @@
+// C ABI of the backward pass: checks, the choice of path, workspace, launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+#include <cstring>
+
+#include "bwd_rows.cuh"
+#include "launch_bwd.h"
+
+namespace sdpa {
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+sdpa_status refuse(sdpa_status st, const char *msg) { return set_error(st, msg); }
+
+sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *out) {
+  BwdPlan pl;
+  memset(&pl, 0, sizeof(pl));
+  pl.rows = (int)((long long)pb.Hq / pb.Hkv * pb.L);
+  const long long rpad = ((long long)pl.rows + 127) / 128 * 128;
+  if (rpad > 0x7fffffffLL) return refuse(SDPA_ERR_UNSUPPORTED, "more than 2^31 - 128 packed query rows per KV head");
+  pl.rpad = (int)rpad;
+  if (force_path != SDPA_BWD_PATH_AUTO && force_path != SDPA_BWD_PATH_TILE)
+    return refuse(SDPA_ERR_INVALID_ARG, "unknown backward path");
+  pl.path = SDPA_BWD_PATH_TILE;
+  const size_t slabs = (size_t)pb.B * pb.Hkv;
+  pl.row_bytes = align256(slabs * pl.rpad * sizeof(float));
+  pl.norm_bytes = align256(slabs * 16);
+  pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes;
+  *out = pl;
+  return SDPA_OK;
+}
+
+struct Range {
+  const void *p;
+  size_t n;
+};
+
+}  // namespace
+}  // namespace sdpa
+
+using namespace sdpa;
+
+static Problem bwd_problem(int B, int Hq, int Hkv, int L, int S, int Dqk, int Dv, float scale,
+                           int causal, int window, sdpa_dtype dtype,
+                           const sdpa_backward_options *opt) {
+  Problem p;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.L = L; p.S = S; p.Dqk = Dqk; p.Dv = Dv;
+  p.scale = scale; p.causal = causal; p.window = window; p.dtype = dtype;
+  p.has_q_offset = opt != nullptr && opt->has_q_offset ? 1 : 0;
+  p.q_offset = p.has_q_offset ? opt->q_offset : S - L;
+  return p;
+}
+
+extern "C" SDPA_API size_t sdpa_backward_workspace_bytes(int B, int Hq, int Hkv, int L, int S,
+                                                         int Dqk, int Dv, int causal,
+                                                         int window_size, sdpa_dtype dtype,
+                                                         const sdpa_backward_options *opt) {
+  set_error(SDPA_OK, "");
+  const Problem pb = bwd_problem(B, Hq, Hkv, L, S, Dqk, Dv, 1.f, causal, window_size, dtype, opt);
+  if (validate_problem(pb) != SDPA_OK) return 0;
+  int sms;
+  unsigned int *wd;
+  uint64_t limit;
+  if (device_info(&sms, &wd, &limit) != SDPA_OK) return 0;
+  BwdPlan pl;
+  if (make_bwd_plan(pb, sms, opt ? opt->force_path : 0, &pl) != SDPA_OK) return 0;
+  return pl.ws_bytes;
+}
+
+extern "C" SDPA_API sdpa_status sdpa_backward(
+    const void *q, const void *k, const void *v, const void *out, const float *lse,
+    const void *dout, void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int L, int S, int Dqk,
+    int Dv, float scale, int causal, int window_size, sdpa_dtype dtype,
+    const sdpa_backward_options *opt, void *workspace, size_t workspace_bytes,
+    sdpa_stream_t stream) {
+  set_error(SDPA_OK, "");
+  const Problem pb = bwd_problem(B, Hq, Hkv, L, S, Dqk, Dv, scale, causal, window_size, dtype, opt);
+  sdpa_status st = validate_problem(pb);
+  if (st != SDPA_OK) return st;
+  const float *sinks = opt ? opt->sinks : nullptr, *dlse = opt ? opt->dlse : nullptr;
+  float *dsinks = opt ? opt->dsinks : nullptr;
+  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)
+    return refuse(SDPA_ERR_INVALID_ARG, "q, k, v, out, lse, dout, dq, dk and dv must be non-NULL device pointers");
+  for (const void *p : {q, k, v, out, dout, (const void *)dq, (const void *)dk, (const void *)dv})
+    if (reinterpret_cast<uintptr_t>(p) & 15u)
+      return refuse(SDPA_ERR_INVALID_ARG, "q, k, v, out, dout, dq, dk and dv must be 16-byte aligned");
+  for (const float *p : {lse, sinks, dlse, (const float *)dsinks})
+    if (reinterpret_cast<uintptr_t>(p) & 3u)
+      return refuse(SDPA_ERR_INVALID_ARG, "lse, sinks, dlse and dsinks must be 4-byte aligned");
+  if (dsinks && !sinks) return refuse(SDPA_ERR_INVALID_ARG, "dsinks needs sinks");
+  const size_t rows = (size_t)B * Hq * L, keys = (size_t)B * Hkv * S;
+  const Range in[] = {{q, rows * Dqk * 2}, {k, keys * Dqk * 2},  {v, keys * Dv * 2}, {out, rows * Dv * 2},
+                      {dout, rows * Dv * 2}, {lse, rows * 4}, {sinks, sinks ? (size_t)Hq * 4 : 0}, {dlse, dlse ? rows * 4 : 0}};
+  const Range to[] = {{dq, rows * Dqk * 2}, {dk, keys * Dqk * 2}, {dv, keys * Dv * 2}, {dsinks, dsinks ? (size_t)Hq * 4 : 0}};
+  for (int i = 0; i < 4; ++i) {
+    if (to[i].n == 0) continue;
+    for (const Range &r : in)
+      if (r.n && extents_meet(to[i].p, to[i].n, r.p, r.n))
+        return refuse(SDPA_ERR_INVALID_ARG, "a gradient must not overlap an input");
+    for (int j = 0; j < i; ++j)
+      if (to[j].n && extents_meet(to[i].p, to[i].n, to[j].p, to[j].n))
+        return refuse(SDPA_ERR_INVALID_ARG, "the gradients must not overlap each other");
+  }
+  const bool own_ws = workspace == nullptr && workspace_bytes == 0;
+  if (!own_ws && (reinterpret_cast<uintptr_t>(workspace) & 15u))
+    return refuse(SDPA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+
+  BwdLaunch ln;
+  memset(&ln, 0, sizeof(ln));
+  st = device_info(&ln.sms, &ln.wd_word, &ln.wd_limit_ns);
+  if (st != SDPA_OK) return st;
+  st = make_bwd_plan(pb, ln.sms, opt ? opt->force_path : 0, &ln.plan);
+  if (st != SDPA_OK) return st;
+  const BwdPlan &pl = ln.plan;
+  const cudaStream_t cs = (cudaStream_t)stream;
+  if (own_ws) {
+    st = pool_alloc(&workspace, pl.ws_bytes, cs, "backward");
+    if (st != SDPA_OK) return st;
+  } else if (workspace == nullptr || workspace_bytes < pl.ws_bytes) {
+    char buf[128];
+    snprintf(buf, sizeof(buf), "workspace of %zu bytes needed, %zu given", pl.ws_bytes,
+             workspace == nullptr ? (size_t)0 : workspace_bytes);
+    return refuse(SDPA_ERR_RESOURCES, buf);
+  }
+  ln.pb = pb;
+  ln.q = q; ln.k = k; ln.v = v; ln.out = out; ln.dout = dout;
+  ln.dq = dq; ln.dk = dk; ln.dv = dv;
+  ln.lse = lse; ln.dlse = dlse;
+  char *ws = static_cast<char *>(workspace);
+  ln.nlse = reinterpret_cast<float *>(ws);
+  ln.ndelta = reinterpret_cast<float *>(ws + pl.row_bytes);
+  ln.norms = reinterpret_cast<unsigned int *>(ws + 2 * pl.row_bytes);
+  ln.stream = cs;
+
+  std::string err;
+  st = launch_bwd_rows(ln, &err);
+  if (st == SDPA_OK) st = launch_bwd_tile(ln, &err);
+  if (st == SDPA_OK && dsinks) {
+    bwd_sinks_kernel<<<Hq, kBwdSinksThreads, 0, cs>>>(sinks, lse, ln.ndelta, dsinks, B, Hq, Hkv, L, pl.rpad);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+      err = std::string("bwd_sinks_kernel launch failed: ") + cudaGetErrorString(e);
+      st = SDPA_ERR_CUDA;
+    }
+  }
+  if (own_ws) {
+    cudaError_t e = cudaFreeAsync(workspace, cs);
+    if (st == SDPA_OK && e != cudaSuccess) {
+      err = std::string("cudaFreeAsync: ") + cudaGetErrorString(e);
+      st = SDPA_ERR_CUDA;
+    }
+  }
+  return st == SDPA_OK ? SDPA_OK : set_error(st, err);
+}
+
+namespace sdpa {
+
+sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err) {
+  const Problem &pb = ln.pb;
+  const long long slabs = (long long)pb.B * pb.Hkv;
+  const bool bf16 = pb.dtype == SDPA_BF16;
+  BwdRowsParams p;
+  p.out = ln.out; p.dout = ln.dout; p.v = ln.v;
+  p.lse = ln.lse; p.dlse = ln.dlse;
+  p.nlse = ln.nlse; p.ndelta = ln.ndelta; p.norms = ln.norms;
+  p.R = ln.plan.rows; p.rpad = ln.plan.rpad; p.S = pb.S; p.Dv = pb.Dv;
+  p.row_ctas = slabs * p.rpad / kBwdRowsPerCta;
+  p.v_ctas = bf16 ? 0 : (pb.S + kBwdRowsPerCta - 1) / kBwdRowsPerCta;
+  const long long ctas = p.row_ctas + slabs * p.v_ctas;
+  if (ctas > 0x7fffffffLL) {
+    *err = "problem needs more than 2^31 CTAs for its row terms";
+    return SDPA_ERR_UNSUPPORTED;
+  }
+  cudaError_t e = cudaSuccess;
+  if (!bf16) e = cudaMemsetAsync(ln.norms, 0, slabs * 16, ln.stream);
+  if (e == cudaSuccess) {
+    if (bf16)
+      bwd_rows_kernel<true><<<(unsigned)ctas, kBwdRowsThreads, 0, ln.stream>>>(p);
+    else
+      bwd_rows_kernel<false><<<(unsigned)ctas, kBwdRowsThreads, 0, ln.stream>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    *err = std::string("bwd_rows_kernel launch failed: ") + cudaGetErrorString(e);
+    return SDPA_ERR_CUDA;
+  }
+  return SDPA_OK;
+}
+
+void fill_bwd_params(const BwdLaunch &ln, BwdParams *p) {
+  const Problem &pb = ln.pb;
+  memset(p, 0, sizeof(*p));
+  AttnParams &a = p->a;
+  a.B = pb.B; a.Hq = pb.Hq; a.Hkv = pb.Hkv; a.L = pb.L; a.S = pb.S; a.Dqk = pb.Dqk; a.Dv = pb.Dv;
+  a.R = ln.plan.rows;
+  a.off = pb.q_offset;
+  a.causal = pb.causal;
+  a.window = pb.window;
+  a.scale_log2 = pb.scale * 1.4426950408889634f;
+  a.splits = 1;
+  a.wd.word = ln.wd_word;
+  a.wd.limit_ns = ln.wd_limit_ns;
+  p->nlse = ln.nlse; p->ndelta = ln.ndelta; p->norms = ln.norms;
+  p->rpad = ln.plan.rpad;
+  p->scale = pb.scale;
+  p->q = ln.q; p->k = ln.k; p->v = ln.v; p->dout = ln.dout;
+  p->dq = ln.dq; p->dk = ln.dk; p->dv = ln.dv;
+}
+
+}  // namespace sdpa

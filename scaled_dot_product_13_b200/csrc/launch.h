@@ -142,12 +142,26 @@ sdpa_status forward_call(const Problem &pb, const void *q, const void *k, const 
 sdpa_status validate_call(const Problem &pb, const void *q, const void *k, const void *v,
                           const void *out);
 
+// The shape checks alone.
+sdpa_status validate_problem(const Problem &pb);
+
 // Id of the calling thread's current CUDA context (unique within the process,
 // never reused), or SDPA_ERR_CUDA when no context is current.
 sdpa_status current_context_id(unsigned long long *id);
 
 // Validate and plan for the current device without enqueuing anything.
 sdpa_status plan_call(const Problem &pb, int force_path, int force_splits, Plan *plan);
+
+// The current device: SM count, watchdog word and the limit of one bounded
+// wait (fails with a message off sm_100a).
+sdpa_status device_info(int *sms, unsigned int **wd_word, uint64_t *wait_limit_ns);
+
+// Stream-ordered workspace of the allocating entry points (honours the test
+// hook that makes it fail).
+sdpa_status pool_alloc(void **ptr, size_t bytes, cudaStream_t stream, const char *what);
+
+// Extents [a, a+na) and [b, b+nb) meet.
+bool extents_meet(const void *a, size_t na, const void *b, size_t nb);
 
 // Record `msg` as this thread's last error and return `st`.
 sdpa_status set_error(sdpa_status st, const std::string &msg);

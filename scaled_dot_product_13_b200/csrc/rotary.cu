@@ -1,0 +1,379 @@
+// Rotary positions (forward and gradient): the plan, the checks, the kernel.
+//
+// Per pair: (a, b) -> m (a cos t - b sin t, a sin t + b cos t), t = position *
+// frequency.  The work is one read and one write of every element, so the
+// kernel is bound by memory traffic; what it must avoid is (1) paying for the
+// angles per head and (2) losing them at far positions.
+//
+// (1) A thread owns V pairs of one token and walks over a group of heads (q's
+// and k's in one list), so one sine and cosine per pair serves the group.
+// (2) Frequencies are 64-bit fixed-point turns per position: position * turns
+// wraps modulo one turn by itself, exactly; the top 32 bits are the angle in
+// 2^-32 turns, converted to half-turns in fp32 (relative error 2^-24) for
+// sincospif.  A float product position * w would be off by 2^-24 * t radians,
+// i.e. 0.008 at position 131072 in the first pair.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace sdpa {
+namespace {
+
+constexpr int kThreads = 256;
+// Heads loaded before the first is computed (loads in flight per thread).
+constexpr int kBatch = 4;
+
+struct RotaryTensor {
+  const uint16_t *x;
+  uint16_t *out;
+  long long xb, xh, xt, ob, oh, ot;
+};
+
+struct RotaryParams {
+  RotaryTensor t[2];
+  int heads0;        // heads of t[0]
+  int heads;         // heads of both
+  int heads_per_cta; // one grid.y
+  int L;
+  long long tokens;  // B * L
+  int rot_items;     // V-pair items of one head
+  int items;         // ... and V-element items copied behind them
+  int half;          // rotary_dim / 2
+  const void *positions;
+  int position_bits;
+  long long position_batch_stride, offset;
+  int inverse;
+  float magnitude;
+  uint64_t turns[256];
+};
+
+template <int V>
+struct Pack {
+  static_assert(V == 1 || V == 2 || V == 4 || V == 8, "");
+};
+template <>
+struct Pack<1> { using type = uint16_t; };
+template <>
+struct Pack<2> { using type = uint32_t; };
+template <>
+struct Pack<4> { using type = uint2; };
+template <>
+struct Pack<8> { using type = uint4; };
+
+template <int V>
+union Elems {
+  typename Pack<V>::type v;
+  uint16_t e[V];
+};
+
+template <bool kBF16>
+__device__ __forceinline__ float widen(uint16_t b) {
+  if constexpr (kBF16) return __uint_as_float((uint32_t)b << 16);
+  return __half2float(__ushort_as_half(b));
+}
+template <bool kBF16>
+__device__ __forceinline__ uint16_t narrow(float f) {
+  if constexpr (kBF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+  return __half_as_ushort(__float2half_rn(f));
+}
+
+template <bool kBF16, bool kInterleaved, int V>
+__global__ void __launch_bounds__(kThreads)
+    rotary_kernel(const __grid_constant__ RotaryParams p) {
+  using T = typename Pack<V>::type;
+  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long token = id / p.items;
+  if (token >= p.tokens) return;
+  const int item = (int)(id - token * p.items);
+  const long long b = token / p.L;
+  const long long l = token - b * p.L;
+  const bool rotated = item < p.rot_items;
+  // the item's two runs of V elements (one, for a copied item)
+  int e0, e1;
+  if (rotated) {
+    e0 = kInterleaved ? 2 * V * item : V * item;
+    e1 = kInterleaved ? e0 + V : e0 + p.half;
+  } else {
+    e0 = 2 * p.half + V * (item - p.rot_items);
+    e1 = e0;
+  }
+  float cs[V], sn[V];
+  if (rotated) {
+    long long pos = l;
+    if (p.position_bits == 64)
+      pos = static_cast<const long long *>(p.positions)[b * p.position_batch_stride + l];
+    else if (p.position_bits == 32)
+      pos = static_cast<const int *>(p.positions)[b * p.position_batch_stride + l];
+    pos += p.offset;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint64_t turn = (uint64_t)pos * p.turns[V * item + i];
+      const float half_turns = (float)(int)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
+      sincospif(half_turns, &sn[i], &cs[i]);
+      cs[i] *= p.magnitude;
+      sn[i] *= p.inverse ? -p.magnitude : p.magnitude;
+    }
+  }
+  const int h_begin = blockIdx.y * p.heads_per_cta;
+  const int h_end = min(h_begin + p.heads_per_cta, p.heads);
+  for (int h0 = h_begin; h0 < h_end; h0 += kBatch) {
+    Elems<V> a[kBatch], c[kBatch];
+    uint16_t *dst[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h0 + u;
+      if (h >= h_end) break;
+      const bool second = h >= p.heads0;
+      const RotaryTensor &t = p.t[second];
+      const long long hh = second ? h - p.heads0 : h;
+      const uint16_t *src = t.x + b * t.xb + hh * t.xh + l * t.xt;
+      dst[u] = t.out + b * t.ob + hh * t.oh + l * t.ot;
+      a[u].v = *reinterpret_cast<const T *>(src + e0);
+      if (rotated) c[u].v = *reinterpret_cast<const T *>(src + e1);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (h0 + u >= h_end) break;
+      if (rotated) {
+        float x[2 * V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          x[i] = widen<kBF16>(a[u].e[i]);
+          x[V + i] = widen<kBF16>(c[u].e[i]);
+        }
+        float y[2 * V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          // pair i: neighbours 2i, 2i+1 of the 2V elements, or i of both runs
+          const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : V + i;
+          y[ia] = x[ia] * cs[i] - x[ib] * sn[i];
+          y[ib] = x[ia] * sn[i] + x[ib] * cs[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          a[u].e[i] = narrow<kBF16>(y[i]);
+          c[u].e[i] = narrow<kBF16>(y[V + i]);
+        }
+        *reinterpret_cast<T *>(dst[u] + e1) = c[u].v;
+      }
+      *reinterpret_cast<T *>(dst[u] + e0) = a[u].v;
+    }
+  }
+}
+
+template <bool kBF16, bool kInterleaved>
+cudaError_t launch_width(int v, dim3 grid, cudaStream_t stream, const RotaryParams &p) {
+  switch (v) {
+    case 8: rotary_kernel<kBF16, kInterleaved, 8><<<grid, kThreads, 0, stream>>>(p); break;
+    case 4: rotary_kernel<kBF16, kInterleaved, 4><<<grid, kThreads, 0, stream>>>(p); break;
+    case 2: rotary_kernel<kBF16, kInterleaved, 2><<<grid, kThreads, 0, stream>>>(p); break;
+    default: rotary_kernel<kBF16, kInterleaved, 1><<<grid, kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+sdpa_status bad(const char *fmt, double a = 0, double b = 0) {
+  char buf[256];
+  snprintf(buf, sizeof(buf), fmt, a, b);
+  return set_error(SDPA_ERR_INVALID_ARG, buf);
+}
+
+// Elements from the first to one past the last of a view, and whether strides
+// keep its elements apart (each stride, in rising order, at least the extent
+// of the dimensions below it).
+long long extent(const sdpa_strides &s, int B, int heads, int L, int D) {
+  return (long long)(B - 1) * s.batch + (long long)(heads - 1) * s.head +
+         (long long)(L - 1) * s.token + D;
+}
+bool apart(const sdpa_strides &s, int B, int heads, int L, int D) {
+  struct Dim { long long stride, size; } d[3] = {{s.batch, B}, {s.head, heads}, {s.token, L}};
+  std::sort(d, d + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+  long long span = D;
+  for (const Dim &x : d) {
+    if (x.size == 1) continue;
+    if (x.stride < span) return false;
+    span = (x.size - 1) * x.stride + span;
+  }
+  return true;
+}
+
+}  // namespace
+}  // namespace sdpa
+
+using namespace sdpa;
+
+extern "C" SDPA_API sdpa_status sdpa_rotary_init(const sdpa_rotary_config *c,
+                                                 sdpa_rotary_plan *plan) {
+  set_error(SDPA_OK, "");
+  if (!c || !plan) return bad("config and plan must be non-NULL");
+  const int R = c->rotary_dim == 0 ? c->head_dim : c->rotary_dim;
+  if (c->head_dim < 2 || c->head_dim > 512)
+    return bad("head_dim must lie in [2, 512] (got %.0f)", c->head_dim);
+  if (R < 2 || R % 2 != 0 || R > c->head_dim)
+    return bad("rotary_dim must be even, in [2, head_dim] (got %.0f of %.0f)", R, c->head_dim);
+  if (c->interleaved != 0 && c->interleaved != 1)
+    return bad("interleaved must be 0 or 1 (got %.0f)", c->interleaved);
+  const double base = c->base == 0 ? 10000.0 : c->base;
+  if (!(base > 1.0) || !std::isfinite(base)) return bad("base must be above 1 (got %g)", base);
+  if (c->scaling < SDPA_ROPE_PLAIN || c->scaling > SDPA_ROPE_BANDED)
+    return bad("unknown scaling %.0f", c->scaling);
+  const bool by_turns = c->scaling == SDPA_ROPE_YARN || c->scaling == SDPA_ROPE_BANDED;
+  if (c->scaling != SDPA_ROPE_PLAIN && !(c->factor > 0 && std::isfinite(c->factor)))
+    return bad("factor must be positive (got %g)", c->factor);
+  if (c->scaling == SDPA_ROPE_NTK && R < 4) return bad("ntk scaling needs rotary_dim >= 4");
+  const double fast = c->beta_fast != 0 ? c->beta_fast : c->scaling == SDPA_ROPE_BANDED ? 4.0 : 32.0;
+  const double slow = c->beta_slow != 0 ? c->beta_slow : 1.0;
+  if (by_turns && c->original_length < 1)
+    return bad("original_length must be >= 1 (got %.0f)", c->original_length);
+  if (by_turns && !(slow > 0 && fast > slow && std::isfinite(fast)))
+    return bad("beta_fast (%g) must be above beta_slow (%g), both positive", fast, slow);
+  if (!std::isfinite(c->magnitude) || c->magnitude < 0)
+    return bad("magnitude must be finite and not negative (got %g)", c->magnitude);
+
+  // In extended precision: an error of 2^-64 relative in a frequency stays
+  // below 2^-32 turns at every 32-bit position.
+  const long double kTwoPi = 6.283185307179586476925286766559L;
+  long double b = base;
+  const long double f = c->scaling == SDPA_ROPE_PLAIN ? 1.0L : (long double)c->factor;
+  if (c->scaling == SDPA_ROPE_NTK) b = b * powl(f, (long double)R / (R - 2));
+  long double lo = 0, hi = 0;  // yarn: pair indices of beta_fast and beta_slow turns
+  if (c->scaling == SDPA_ROPE_YARN) {
+    lo = floorl(R * logl(c->original_length / (fast * kTwoPi)) / (2 * logl(b)));
+    hi = ceill(R * logl(c->original_length / (slow * kTwoPi)) / (2 * logl(b)));
+    lo = std::max(lo, 0.0L);
+    hi = std::min(hi, (long double)(R - 1));
+  }
+  memset(plan, 0, sizeof(*plan));
+  for (int i = 0; i < R / 2; ++i) {
+    long double w = powl(b, -2.0L * i / R);
+    long double keep = 1;
+    switch (c->scaling) {
+      case SDPA_ROPE_LINEAR: keep = 0; break;
+      case SDPA_ROPE_YARN: keep = 1 - std::min(std::max((i - lo) / std::max(hi - lo, 0.001L), 0.0L), 1.0L); break;
+      case SDPA_ROPE_BANDED:
+        keep = std::min(std::max((c->original_length * w / kTwoPi - slow) / (fast - slow), 0.0L), 1.0L);
+        break;
+    }
+    w = w * keep + w / f * (1 - keep);
+    long double turns = w / kTwoPi;
+    turns -= floorl(turns);
+    // to the nearest 2^-64 of a turn; a whole turn is none
+    const long double fixed = roundl(ldexpl(turns, 64));
+    plan->turns[i] = fixed >= ldexpl(1.0L, 64) ? 0 : (uint64_t)fixed;
+  }
+  plan->head_dim = c->head_dim;
+  plan->rotary_dim = R;
+  plan->interleaved = c->interleaved;
+  plan->magnitude = c->magnitude != 0                ? (float)c->magnitude
+                    : c->scaling == SDPA_ROPE_YARN && f > 1 ? (float)(0.1L * logl(f) + 1)
+                                                     : 1.0f;
+  return SDPA_OK;
+}
+
+extern "C" SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan,
+                                            const sdpa_rotary_tensor *tensors, int count, int B,
+                                            int L, const void *positions, int position_bits,
+                                            long long position_batch_stride, long long offset,
+                                            int inverse, sdpa_dtype dtype, sdpa_stream_t stream) {
+  set_error(SDPA_OK, "");
+  if (!plan || !tensors) return bad("plan and tensors must be non-NULL");
+  if (count != 1 && count != 2) return bad("count must be 1 or 2 (got %.0f)", count);
+  const int D = plan->head_dim, R = plan->rotary_dim;
+  if (D < 2 || D > 512 || R < 2 || R > D || R % 2 != 0 ||
+      (plan->interleaved != 0 && plan->interleaved != 1))
+    return bad("the plan was not filled by sdpa_rotary_init");
+  if (dtype != SDPA_BF16 && dtype != SDPA_F16)
+    return set_error(SDPA_ERR_UNSUPPORTED, "dtype is not supported (bf16 = 0, f16 = 1)");
+  if (B < 1 || L < 1) return bad("B and L must be >= 1 (got B=%.0f L=%.0f)", B, L);
+  if ((long long)B * L > 0x7fffffffLL)
+    return set_error(SDPA_ERR_UNSUPPORTED, "B*L must stay below 2^31");
+  if (inverse != 0 && inverse != 1) return bad("inverse must be 0 or 1 (got %.0f)", inverse);
+  if (positions ? (position_bits != 32 && position_bits != 64) : position_bits != 0)
+    return bad("position_bits must be 32 or 64 with positions, 0 without (got %.0f)", position_bits);
+  if (positions && ((reinterpret_cast<uintptr_t>(positions) & (position_bits / 8 - 1)) != 0 ||
+                    position_batch_stride < 0))
+    return bad("positions must be aligned to their type, with a batch stride >= 0");
+
+  RotaryParams p;
+  memset(&p, 0, sizeof(p));
+  // Widest run of elements that every row, run and pitch is a multiple of:
+  // 16-byte accesses for the common head dims (measured against 2-byte ones at
+  // the prompt case: see the notes at the launch below).
+  int v = 8;
+  auto fit = [&v](unsigned long long x) {
+    while (x % v != 0) v >>= 1;
+  };
+  fit(R / 2);
+  fit(D);
+  for (int i = 0; i < count; ++i) {
+    const sdpa_rotary_tensor &t = tensors[i];
+    if (!t.x || !t.out) return bad("x and out must be non-NULL device pointers");
+    if (t.heads < 1) return bad("heads must be >= 1 (got %.0f)", t.heads);
+    if ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.out)) & 1u)
+      return bad("x and out must be 2-byte aligned");
+    // the stride of a dimension of one element is never used
+    auto used = [&](sdpa_strides s) {
+      if (B == 1) s.batch = 0;
+      if (t.heads == 1) s.head = 0;
+      if (L == 1) s.token = 0;
+      return s;
+    };
+    const sdpa_strides xs = used(t.x_strides), os = used(t.out_strides);
+    for (long long st : {xs.batch, xs.head, xs.token, os.batch, os.head, os.token})
+      if (st < 0 || st > (1LL << 40)) return bad("strides must lie in [0, 2^40] (got %.0f)", (double)st);
+    if (!apart(os, B, t.heads, L, D))
+      return bad("out strides must keep the rows of head_dim elements apart");
+    const bool same = t.x == t.out && xs.batch == os.batch && xs.head == os.head && xs.token == os.token;
+    if (!same && extents_meet(t.x, 2 * extent(xs, B, t.heads, L, D), t.out, 2 * extent(os, B, t.heads, L, D)))
+      return bad("out must be x itself or not overlap it");
+    fit(reinterpret_cast<uintptr_t>(t.x) / 2);
+    fit(reinterpret_cast<uintptr_t>(t.out) / 2);
+    for (long long st : {xs.batch, xs.head, xs.token, os.batch, os.head, os.token}) fit((unsigned long long)st);
+    p.t[i] = {static_cast<const uint16_t *>(t.x), static_cast<uint16_t *>(t.out),
+              xs.batch, xs.head, xs.token, os.batch, os.head, os.token};
+    p.heads += t.heads;
+    if (p.heads > 0xffff) return set_error(SDPA_ERR_UNSUPPORTED, "more than 65535 heads in one call");
+  }
+  int sms;
+  unsigned int *wd;
+  uint64_t limit;
+  sdpa_status st = device_info(&sms, &wd, &limit);
+  if (st != SDPA_OK) return st;
+
+  p.heads0 = tensors[0].heads;
+  p.L = L;
+  p.tokens = (long long)B * L;
+  p.rot_items = R / 2 / v;
+  p.items = p.rot_items + (D - R) / v;
+  p.half = R / 2;
+  p.positions = positions;
+  p.position_bits = position_bits;
+  p.position_batch_stride = position_batch_stride;
+  p.offset = offset;
+  p.inverse = inverse;
+  p.magnitude = plan->magnitude;
+  memcpy(p.turns, plan->turns, sizeof(p.turns));
+  // Heads per thread: as many as leave two full waves of threads, so that the
+  // angles are shared; all in their own threads for a few tokens.
+  const long long threads = p.tokens * p.items;
+  const long long want = 2LL * sms * 2048;
+  long long groups = std::min<long long>(p.heads, (want + threads - 1) / threads);
+  p.heads_per_cta = (int)((p.heads + groups - 1) / groups);
+  groups = (p.heads + p.heads_per_cta - 1) / p.heads_per_cta;
+  const long long ctas = (threads + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffLL) return set_error(SDPA_ERR_UNSUPPORTED, "too many tokens for one launch");
+  const dim3 grid((unsigned)ctas, (unsigned)groups);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const bool il = plan->interleaved != 0;
+  cudaError_t e = dtype == SDPA_BF16 ? (il ? launch_width<true, true>(v, grid, cs, p) : launch_width<true, false>(v, grid, cs, p))
+                                     : (il ? launch_width<false, true>(v, grid, cs, p) : launch_width<false, false>(v, grid, cs, p));
+  if (e != cudaSuccess)
+    return set_error(SDPA_ERR_CUDA, std::string("rotary_kernel launch failed: ") + cudaGetErrorString(e));
+  return SDPA_OK;
+}

@@ -1,0 +1,125 @@
+"""Rotary positions: the plan's frequencies against the formulas in exact
+arithmetic, and every refusal (CPU; no kernel is launched)."""
+import ctypes
+import math
+from fractions import Fraction
+
+import pytest
+
+import scaled_dot_product_13_b200 as sdpa
+
+TWO_PI = 6.283185307179586476925286766559
+
+
+def _turns(plan):
+    return [plan.turns[i] for i in range(plan.rotary_dim // 2)]
+
+
+def _expected(R, base=10000.0, scaling="none", factor=1.0, orig=0, fast=None, slow=1.0):
+    """Frequencies in turns per position, in double precision."""
+    if scaling == "ntk":
+        base = base * factor ** (R / (R - 2))
+    got = []
+    for i in range(R // 2):
+        w = base ** (-2.0 * i / R)
+        keep = 1.0
+        if scaling == "linear":
+            keep = 0.0
+        elif scaling == "yarn":
+            lo = max(math.floor(R * math.log(orig / ((fast or 32.0) * TWO_PI)) / (2 * math.log(base))), 0)
+            hi = min(math.ceil(R * math.log(orig / (slow * TWO_PI)) / (2 * math.log(base))), R - 1)
+            keep = 1 - min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+        elif scaling == "banded":
+            keep = min(max((orig * w / TWO_PI - slow) / ((fast or 4.0) - slow), 0.0), 1.0)
+        got.append((w * keep + w / factor * (1 - keep)) / TWO_PI)
+    return got
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(base=500000.0), dict(scaling="linear", factor=4.0),
+    dict(scaling="ntk", factor=8.0), dict(scaling="yarn", factor=4.0, original_length=2048),
+    dict(scaling="banded", factor=8.0, original_length=8192),
+    dict(scaling="yarn", factor=2.0, original_length=4096, beta_fast=16.0, beta_slow=2.0),
+])
+@pytest.mark.parametrize("R", [4, 64, 72, 128, 512])
+def test_plan_frequencies(R, kw):
+    plan = sdpa.rotary_plan(512, rotary_dim=R, **kw)
+    want = _expected(R, kw.get("base", 10000.0), kw.get("scaling", "none"), kw.get("factor", 1.0),
+                     kw.get("original_length", 0), kw.get("beta_fast"), kw.get("beta_slow", 1.0))
+    for t, w in zip(_turns(plan), want):
+        # the oracle is in doubles: a few roundings of 2^-53, log and pow; the
+        # plan holds the nearest multiple of 2^-64, at most 2^-65 away
+        assert abs(t / 2.0 ** 64 - w) <= 64 * 2.0 ** -53 * w + 2.0 ** -65
+
+
+def test_first_pair_is_exact_to_the_last_bit():
+    # one radian per position, in turns: 1 / (2 pi), from 40 digits of pi
+    pi = Fraction(3141592653589793238462643383279502884197, 10 ** 39)
+    want = 1 / (2 * pi) * 2 ** 64
+    assert abs(_turns(sdpa.rotary_plan(64))[0] - want) <= 2  # the long double's own 2^-64
+
+
+def test_magnitude():
+    assert sdpa.rotary_plan(64).magnitude == 1.0
+    m = sdpa.rotary_plan(64, scaling="yarn", factor=4.0, original_length=2048).magnitude
+    assert abs(m - (0.1 * math.log(4.0) + 1)) < 1e-7
+    assert sdpa.rotary_plan(64, scaling="yarn", factor=4.0, original_length=2048, magnitude=1.0).magnitude == 1.0
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(head_dim=0), "head_dim"), (dict(head_dim=514), "head_dim"),
+    (dict(head_dim=64, rotary_dim=33), "rotary_dim"), (dict(head_dim=64, rotary_dim=66), "rotary_dim"),
+    (dict(head_dim=64, rotary_dim=-2), "rotary_dim"), (dict(head_dim=64, rotary_dim=0), "rotary_dim"),
+    (dict(head_dim=65), "rotary_dim"),
+    (dict(head_dim=64, base=1.0), "base"), (dict(head_dim=64, base=float("nan")), "base"),
+    (dict(head_dim=64, scaling="other"), "scaling"),
+    (dict(head_dim=64, scaling="linear", factor=0.0), "factor"),
+    (dict(head_dim=64, scaling="linear", factor=float("inf")), "factor"),
+    (dict(head_dim=64, scaling="yarn", factor=2.0), "original_length"),
+    (dict(head_dim=64, scaling="banded", factor=2.0, original_length=2048, beta_fast=1.0), "beta_fast"),
+    (dict(head_dim=64, scaling="ntk", factor=2.0, rotary_dim=2), "ntk"),
+    (dict(head_dim=64, magnitude=-1.0), "magnitude"),
+])
+def test_plan_refusals(kw, words):
+    with pytest.raises(sdpa.SdpaError) as ei:
+        sdpa.rotary_plan(**kw)
+    assert ei.value.status == 1 and words in ei.value.message
+
+
+def _call(plan=None, x=0x10000, out=0x900000, heads=2, xs=(512, 256, 64), os_=(512, 256, 64), count=1, B=2, L=4,
+          pos=None, bits=0, pstride=0, inverse=0, dtype=0):
+    lib = sdpa.load_library()
+    plan = plan or sdpa.rotary_plan(64)
+    t = (sdpa.RotaryTensor * 2)()
+    t[0] = sdpa.RotaryTensor(x, out, heads, sdpa.Strides(*xs), sdpa.Strides(*os_))
+    st = lib.sdpa_rotary(ctypes.byref(plan), t, count, B, L, pos, bits, pstride, 0, inverse, dtype, None)
+    return st, lib.sdpa_last_error_message().decode()
+
+
+@pytest.mark.parametrize("kw,status,words", [
+    (dict(plan=sdpa.RotaryPlan()), 1, "not filled"),
+    (dict(count=0), 1, "count"), (dict(count=3), 1, "count"), (dict(count=2), 1, "non-NULL"),
+    (dict(x=None), 1, "non-NULL"), (dict(out=None), 1, "non-NULL"), (dict(x=0x10001), 1, "2-byte"),
+    (dict(heads=0), 1, "heads"), (dict(B=0), 1, ">= 1"), (dict(L=0), 1, ">= 1"),
+    (dict(inverse=2), 1, "inverse"), (dict(dtype=7), 2, "dtype"),
+    (dict(pos=0x5000, bits=16), 1, "position_bits"), (dict(pos=None, bits=32), 1, "position_bits"),
+    (dict(pos=0x5004, bits=64), 1, "aligned"), (dict(pos=0x5000, bits=64, pstride=-1), 1, "stride"),
+    (dict(xs=(-512, 256, 64)), 1, "strides"),
+    (dict(os_=(512, 256, 0)), 1, "apart"), (dict(os_=(256, 256, 64)), 1, "apart"), (dict(os_=(512, 256, 63)), 1, "apart"),
+    (dict(out=0x10000 + 128), 1, "overlap"), (dict(out=0x10000, xs=(512, 64, 128)), 1, "overlap"),
+    (dict(B=1 << 16, L=1 << 16), 2, "2^31"),
+])
+def test_call_refusals_before_any_cuda_call(kw, status, words):
+    st, msg = _call(**kw)
+    assert st == status and words in msg, (st, msg)
+
+
+def test_python_checks():
+    torch = pytest.importorskip("torch")
+    plan = sdpa.rotary_plan(64)
+    with pytest.raises(sdpa.SdpaError, match="CUDA tensor"):
+        sdpa.rotary(plan, torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16))
+    with pytest.raises(sdpa.SdpaError, match="must be"):
+        sdpa.rotary(plan, torch.zeros(2, 3, 64, dtype=torch.bfloat16))
+    with pytest.raises(sdpa.SdpaError, match="rotary_plan"):
+        sdpa.rotary(None, torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16))

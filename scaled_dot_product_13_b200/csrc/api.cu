@@ -623,8 +623,8 @@ sdpa_status set_error(sdpa_status st, const std::string &msg) { return fail_str(
 namespace {
 // Recently encoded tensor maps of this host thread.  A descriptor depends only
 // on its arguments (no device state), so an eager loop of calls on the same
-// tensors reuses it instead of encoding it again; a few entries cover Q, K
-// and V of the last calls.
+// tensors reuses it instead of encoding it again; a few entries cover the
+// last calls (a backward call has up to eleven).
 struct TmaCacheEntry {
   bool used;
   int dt;  // CUtensorMapDataType
@@ -634,7 +634,7 @@ struct TmaCacheEntry {
   uint32_t box[3];
   CUtensorMap map;
 };
-constexpr int kTmaCacheSize = 12;
+constexpr int kTmaCacheSize = 24;
 thread_local TmaCacheEntry t_tma_cache[kTmaCacheSize];
 thread_local int t_tma_next = 0;
 

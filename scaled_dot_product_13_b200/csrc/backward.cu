@@ -15,20 +15,56 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 sdpa_status refuse(sdpa_status st, const char *msg) { return set_error(st, msg); }
 
+// Blocks each part of a split tile keeps at least: below that its operand
+// loads and its share of the join cost more than the parallelism gives.
+constexpr int kMinBlocksPerPart = 4;
+
 sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *out) {
   BwdPlan pl;
   memset(&pl, 0, sizeof(pl));
-  pl.rows = (int)((long long)pb.Hq / pb.Hkv * pb.L);
-  const long long rpad = ((long long)pl.rows + 127) / 128 * 128;
-  if (rpad > 0x7fffffffLL) return refuse(SDPA_ERR_UNSUPPORTED, "more than 2^31 - 128 packed query rows per KV head");
-  pl.rpad = (int)rpad;
-  if (force_path != SDPA_BWD_PATH_AUTO && force_path != SDPA_BWD_PATH_TILE)
+  const long long rows = (long long)pb.Hq / pb.Hkv * pb.L;
+  const long long kMax = 0x7fffffffLL - 1024;  // tile and block ends stay in 32 bits
+  if (rows > kMax || pb.S > kMax)
+    return refuse(SDPA_ERR_UNSUPPORTED, "more than 2^31 - 1025 packed query rows per KV head, or keys");
+  pl.rows = (int)rows;
+  if (force_path != SDPA_BWD_PATH_AUTO && force_path != SDPA_BWD_PATH_TILE && force_path != SDPA_BWD_PATH_TC)
     return refuse(SDPA_ERR_INVALID_ARG, "unknown backward path");
-  pl.path = SDPA_BWD_PATH_TILE;
+  pl.pair = 0;
+  while (pl.pair < kNumDimPairs && (kDimPairs[pl.pair].dqk < pb.Dqk || kDimPairs[pl.pair].dv < pb.Dv)) ++pl.pair;
+  const bool tc_fits = pl.pair < kWidePair && rows < (1 << 30) && pb.S < (1 << 30);
+  if (force_path == SDPA_BWD_PATH_TC && !tc_fits)
+    return refuse(SDPA_ERR_UNSUPPORTED, "the tcgen05 backward path is built for head dims up to 256 and up to 2^30 rows and keys");
+  pl.path = force_path != SDPA_BWD_PATH_AUTO ? force_path : tc_fits ? SDPA_BWD_PATH_TC : SDPA_BWD_PATH_TILE;
+  pl.rpad = (pl.rows + 127) / 128 * 128;
+  pl.key_splits = pl.row_splits = 1;
   const size_t slabs = (size_t)pb.B * pb.Hkv;
+  if (pl.path == SDPA_BWD_PATH_TC) {
+    const DimPair dp = kDimPairs[pl.pair];
+    const int bn = bwd_tc_block(pl.pair);
+    if (128 % bn != 0) pl.rpad += 128;  // 96-row blocks end up to 95 rows behind the slab
+    // Split a tile's block list where one tile would outlast the whole grid's
+    // work spread over the SMs (few tiles with long lists: few query rows over
+    // many keys, or one KV head under many rows).  Work in block products: 4
+    // for a key tile's block, 3 for a query tile's.
+    const long long kt = (pb.S + 127) / 128, rt = (pl.rows + 127) / 128;
+    const long long kb = (pl.rows + bn - 1) / bn, rb = (pb.S + bn - 1) / bn;
+    const long long ideal = std::max<long long>(1, (long long)slabs * (kt * kb * 4 + rt * rb * 3) / sms);
+    auto parts = [&](long long blocks, int products) {
+      const long long want = (blocks * products + ideal - 1) / ideal;
+      return (int)std::max<long long>(1, std::min(want, blocks / kMinBlocksPerPart));
+    };
+    pl.key_splits = parts(kb, 4);
+    pl.row_splits = parts(rb, 3);
+    if (pl.key_splits > 1) {
+      pl.key_part1_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dqk * sizeof(float));
+      pl.key_part2_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dv * sizeof(float));
+    }
+    if (pl.row_splits > 1)
+      pl.row_part_bytes = align256((size_t)pl.row_splits * slabs * pl.rows * dp.dqk * sizeof(float));
+  }
   pl.row_bytes = align256(slabs * pl.rpad * sizeof(float));
   pl.norm_bytes = align256(slabs * 16);
-  pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes;
+  pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes + pl.key_part1_bytes + pl.key_part2_bytes + pl.row_part_bytes;
   *out = pl;
   return SDPA_OK;
 }
@@ -133,11 +169,15 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
   ln.nlse = reinterpret_cast<float *>(ws);
   ln.ndelta = reinterpret_cast<float *>(ws + pl.row_bytes);
   ln.norms = reinterpret_cast<unsigned int *>(ws + 2 * pl.row_bytes);
+  ws += 2 * pl.row_bytes + pl.norm_bytes;
+  ln.key_part1 = reinterpret_cast<float *>(ws);
+  ln.key_part2 = reinterpret_cast<float *>(ws + pl.key_part1_bytes);
+  ln.row_part = reinterpret_cast<float *>(ws + pl.key_part1_bytes + pl.key_part2_bytes);
   ln.stream = cs;
 
   std::string err;
   st = launch_bwd_rows(ln, &err);
-  if (st == SDPA_OK) st = launch_bwd_tile(ln, &err);
+  if (st == SDPA_OK) st = pl.path == SDPA_BWD_PATH_TC ? launch_bwd_tc(ln, &err) : launch_bwd_tile(ln, &err);
   if (st == SDPA_OK && dsinks) {
     bwd_sinks_kernel<<<Hq, kBwdSinksThreads, 0, cs>>>(sinks, lse, ln.ndelta, dsinks, B, Hq, Hkv, L, pl.rpad);
     cudaError_t e = cudaGetLastError();

@@ -57,6 +57,8 @@ __device__ __forceinline__ void block_max_to(unsigned int *cell, float x, unsign
 template <bool kBF16>
 __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRowsParams p) {
   __shared__ unsigned int tmp[kBwdRowsThreads / 32];
+  // the main kernel may set up now (it waits for this grid)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int sub = threadIdx.x & 7, local = threadIdx.x >> 3;
   const int chunks = p.Dv / 8;
   if (blockIdx.x < p.row_ctas) {

@@ -10,8 +10,12 @@ struct BwdParams;
 struct BwdPlan {
   int path;   // an sdpa_backward_path value other than AUTO
   int rows;   // packed query rows per (batch, KV head)
-  int rpad;   // ... rounded up to 128
-  size_t row_bytes, norm_bytes, ws_bytes;
+  int rpad;   // ... rounded up so that every tile and block stays inside
+  int pair;   // tcgen05 path: index into kDimPairs
+  int key_splits, row_splits;  // parts of a key / query tile's block list
+  size_t row_bytes, norm_bytes;
+  size_t key_part1_bytes, key_part2_bytes, row_part_bytes;  // fp32 sums of the parts
+  size_t ws_bytes;
 };
 
 struct BwdLaunch {
@@ -22,6 +26,7 @@ struct BwdLaunch {
   const float *lse, *dlse;
   float *nlse, *ndelta;
   unsigned int *norms;
+  float *key_part1, *key_part2, *row_part;
   int sms;
   unsigned int *wd_word;
   uint64_t wd_limit_ns;
@@ -33,5 +38,11 @@ void fill_bwd_params(const BwdLaunch &ln, BwdParams *p);
 
 sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err);
 sdpa_status launch_bwd_tile(const BwdLaunch &ln, std::string *err);
+sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err);
+
+// Y rows per block of the tcgen05 path's tiles (index into kDimPairs, up to 5).
+constexpr int bwd_tc_block(int pair) {
+  return kDimPairs[pair].dqk <= 128 ? 128 : kDimPairs[pair].dv <= 128 ? 96 : 64;
+}
 
 }  // namespace sdpa

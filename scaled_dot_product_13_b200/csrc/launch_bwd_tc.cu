@@ -1,0 +1,107 @@
+// Launch unit of the tcgen05 backward kernel and its join.
+#include "bwd_tc.cuh"
+#include "launch_bwd.h"
+
+namespace sdpa {
+
+namespace {
+
+template <bool kBF16>
+cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const float *part, void *out, int rows_per_slab,
+                 int d, int dpad, int splits, int is_dv) {
+  const long long rows = (long long)ln.pb.B * ln.pb.Hkv * rows_per_slab;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows * (d / 4) + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = ln.stream;
+  return cudaLaunchKernelEx(&cfg, bwd_join_kernel<kBF16>, p, part, (uint16_t *)out, rows, rows_per_slab, d,
+                            dpad, splits, is_dv);
+}
+
+template <bool kBF16, int DQK, int DV>
+sdpa_status run(const BwdLaunch &ln, std::string *err) {
+  using Roles = BwdTcRoles<DQK, DV>;
+  auto kern = bwd_tc_kernel<kBF16, DQK, DV>;
+  sdpa_status st = prepare_kernel((const void *)kern, kBwdTcThreads, Roles::kSmem, "bwd_tc_kernel", err);
+  if (st != SDPA_OK) return st;
+  const Problem &pb = ln.pb;
+  const BwdPlan &pl = ln.plan;
+  BwdParams p;
+  fill_bwd_params(ln, &p);
+  const long long slabs = (long long)pb.B * pb.Hkv;
+  BwdTcSpan keys = {(pb.S + 127) / 128, pl.key_splits, pl.key_splits > 1 ? ln.key_part1 : nullptr,
+                    pl.key_splits > 1 ? ln.key_part2 : nullptr};
+  BwdTcSpan rows = {(pl.rows + 127) / 128, pl.row_splits, pl.row_splits > 1 ? ln.row_part : nullptr, nullptr};
+  const long long key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
+  const long long ctas = key_ctas * (Roles::kKinds - 1) + row_ctas;
+  const long long join_ctas = slabs * (pb.S > pl.rows ? (long long)pb.S : pl.rows) * 64 / 256;
+  if (ctas > 0x7fffffffLL || join_ctas > 0x7fffffffLL) {
+    *err = "problem needs more than 2^31 CTAs";
+    return SDPA_ERR_UNSUPPORTED;
+  }
+  auto map = [&](CUtensorMap *m, const void *base, int d, int n, int box_rows) {
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)n, (uint64_t)slabs};
+    const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)n * d * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+    return encode_tma(m, pb.dtype, 3, base, dims, strides, box, err);
+  };
+  constexpr int BN = Roles::BN;
+  const int R = pl.rows, S = pb.S, Dqk = pb.Dqk, Dv = pb.Dv;
+  BwdTcMaps tm;
+  if (!map(&tm.kx, ln.k, Dqk, S, 128) || !map(&tm.vx, ln.v, Dv, S, 128) ||
+      !map(&tm.qy, ln.q, Dqk, R, BN) || !map(&tm.doy, ln.dout, Dv, R, BN) ||
+      !map(&tm.qx, ln.q, Dqk, R, 128) || !map(&tm.dox, ln.dout, Dv, R, 128) ||
+      !map(&tm.ky, ln.k, Dqk, S, BN) || !map(&tm.vy, ln.v, Dv, S, BN) ||
+      !map(&tm.dq, ln.dq, Dqk, R, 128) || !map(&tm.dk, ln.dk, Dqk, S, 128) ||
+      !map(&tm.dv, ln.dv, Dv, S, 128))
+    return SDPA_ERR_CUDA;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kBwdTcThreads);
+  cfg.dynamicSmemBytes = Roles::kSmem;
+  cfg.stream = ln.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm, p, keys, rows);
+  if (e == cudaSuccess && pl.key_splits > 1)
+    e = join<kBF16>(ln, p, keys.part1, ln.dk, S, Dqk, DQK, pl.key_splits, 0);
+  if (e == cudaSuccess && pl.key_splits > 1)
+    e = join<kBF16>(ln, p, keys.part2, ln.dv, S, Dv, DV, pl.key_splits, 1);
+  if (e == cudaSuccess && pl.row_splits > 1)
+    e = join<kBF16>(ln, p, rows.part1, ln.dq, R, Dqk, DQK, pl.row_splits, 0);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    *err = std::string("bwd_tc_kernel launch failed: ") + cudaGetErrorString(e);
+    return SDPA_ERR_CUDA;
+  }
+  return SDPA_OK;
+}
+
+template <bool kBF16>
+sdpa_status run_dtype(const BwdLaunch &ln, std::string *err) {
+  static_assert(BwdTcRoles<128, 128>::BN == bwd_tc_block(2) && BwdTcRoles<192, 128>::BN == bwd_tc_block(3) &&
+                    BwdTcRoles<192, 192>::BN == bwd_tc_block(4) && BwdTcRoles<256, 256>::BN == bwd_tc_block(5),
+                "the plan's blocks are the kernel's");
+  switch (ln.plan.pair) {
+    case 0: return run<kBF16, 64, 64>(ln, err);
+    case 1: return run<kBF16, 80, 80>(ln, err);
+    case 2: return run<kBF16, 128, 128>(ln, err);
+    case 3: return run<kBF16, 192, 128>(ln, err);
+    case 4: return run<kBF16, 192, 192>(ln, err);
+    case 5: return run<kBF16, 256, 256>(ln, err);
+  }
+  *err = "internal: no tcgen05 backward instance for this head-dim pair";
+  return SDPA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err) {
+  return ln.pb.dtype == SDPA_BF16 ? run_dtype<true>(ln, err) : run_dtype<false>(ln, err);
+}
+
+}  // namespace sdpa

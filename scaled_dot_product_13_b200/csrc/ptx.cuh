@@ -410,6 +410,13 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
   return *reinterpret_cast<float2 *>(&d);
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
 
 // 2^x on the FMA and integer pipes, for two values at once (x <= 126).
 // Range reduction in the Cody-Waite style: n = round(x) with the 1.5 * 2^23

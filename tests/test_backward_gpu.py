@@ -8,7 +8,7 @@ from tests import bwd_oracle as O
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
-PATHS = ["tile"]
+PATHS = ["tile", "tc"]
 
 
 def run(sdpa, m, path="auto", **kw):

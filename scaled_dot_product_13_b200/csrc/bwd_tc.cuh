@@ -23,7 +23,7 @@
 //        of a lane need no exchange.
 //   8    TMA producer (X once, then Y1 and Y2 blocks through two rings, the row
 //        terms of a query block with its Y1)
-//   9    MMA issuer (one thread), in the order
+//   9    MMA issuer (the whole warp, one elected lane), in the order
 //            out2_j, S_{j+1}   after P_j   (runs under phase F of block j)
 //            out1_j, dP_{j+1}  after dS_j  (runs under phase E of block j+1)
 //        so the tensor pipe works on one pair while the softmax warps work on
@@ -314,12 +314,16 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     }
   } else if (warp == kMmaWarp) {
     // ============================ MMA issuer ============================
-    if (lane == 0) {
+    // the whole warp, converged: see tc_mma_ss_warp
+    {
       constexpr uint32_t kIdescS = umma_idesc_f16(kBF16, 128, BN, false, false);
       constexpr uint32_t kIdesc1 = umma_idesc_f16(kBF16, 128, Role::D1, false, true);
       constexpr uint32_t kIdesc2 = umma_idesc_f16(kBF16, 128, Role::D2, false, true);
       const uint32_t x1 = smem_u32(sX1), x2 = smem_u32(sX2), y1 = smem_u32(sY1), y2 = smem_u32(sY2);
-      bool ok = mbar_wait(x_full, 0, a.wd, kWdTmaFull);
+      auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t code) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wd, code));
+      };
+      bool ok = wait(x_full, 0, kWdTmaFull);
       // first products: 128 x BN scores over the head dim, both K-major
       auto first = [&](uint32_t x, uint32_t y, int steps, uint32_t col) {
         tc_fence_after();
@@ -327,7 +331,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         const uint64_t b0 = umma_desc_sw128(y, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < steps; ++ks)
-          tc_mma_ss(tmem + col, umma_desc_advance(a0, (ks >> 2) * (128 * 128) + (ks & 3) * 32),
+          tc_mma_ss_warp(tmem + col, umma_desc_advance(a0, (ks >> 2) * (128 * 128) + (ks & 3) * 32),
                     umma_desc_advance(b0, (ks >> 2) * (BN * 128) + (ks & 3) * 32), kIdescS,
                     ks > 0 ? 1u : 0u);
       };
@@ -339,23 +343,23 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
 #pragma unroll
         for (int ks = 0; ks < BN / 16; ++ks) {
           const int half = ks / (kH / 16);
-          tc_mma_ts(tmem + out, tmem + wcol + half * kH + (ks - half * (kH / 16)) * 8,
+          tc_mma_ts_warp(tmem + out, tmem + wcol + half * kH + (ks - half * (kH / 16)) * 8,
                     umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 ? 0u : 1u);
         }
       };
       auto issue_s = [&](int n) -> bool {
         const int s1 = n % N1;
-        if (!mbar_wait(&y1_full[s1], (uint32_t)(n / N1) & 1u, a.wd, kWdTmaFull)) return false;
+        if (!wait(&y1_full[s1], (uint32_t)(n / N1) & 1u, kWdTmaFull)) return false;
         first(x1, y1 + s1 * Role::kY1Bytes, Role::D1 / 16, 0);
-        tc_commit(s_full);
+        tc_commit_warp(s_full);
         return true;
       };
       auto issue_dp = [&](int n) -> bool {
         const int s2 = n % N2;
-        if (!mbar_wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, a.wd, kWdTmaFull)) return false;
+        if (!wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull)) return false;
         first(x2, y2 + s2 * Role::kY2Bytes, Role::D2 / 16, BN);
-        tc_commit(dp_full);
-        if constexpr (!OUT2) tc_commit(&y2_empty[s2]);
+        tc_commit_warp(dp_full);
+        if constexpr (!OUT2) tc_commit_warp(&y2_empty[s2]);
         return true;
       };
       int n = 0;
@@ -368,28 +372,28 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         b = walk.at_or_after(b + 1);
         const bool more = b >= 0 && n + 1 < count;
         const int s1 = n % N1, s2 = n % N2;
-        if (!(ok = mbar_wait(p_full, (uint32_t)n & 1u, a.wd, kWdSoftmax))) break;
+        if (!(ok = wait(p_full, (uint32_t)n & 1u, kWdSoftmax))) break;
         if constexpr (OUT2) {
           if constexpr (!OUT1)
-            if (!(ok = mbar_wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, a.wd, kWdTmaFull))) break;
+            if (!(ok = wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull))) break;
           second(0, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
-          tc_commit(&y2_empty[s2]);
+          tc_commit_warp(&y2_empty[s2]);
           // (not after S_j: the softmax warps read the row terms of the slot)
-          if constexpr (!OUT1) tc_commit(&y1_empty[s1]);
+          if constexpr (!OUT1) tc_commit_warp(&y1_empty[s1]);
         }
         if (more && !(ok = issue_s(n + 1))) break;
         if constexpr (OUT1) {
-          if (!(ok = mbar_wait(ds_full, (uint32_t)n & 1u, a.wd, kWdSoftmax))) break;
+          if (!(ok = wait(ds_full, (uint32_t)n & 1u, kWdSoftmax))) break;
           second(BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
-          tc_commit(&y1_empty[s1]);
+          tc_commit_warp(&y1_empty[s1]);
           if (more && !(ok = issue_dp(n + 1))) break;
         }
         ++n;
         if (!more) break;
       }
-      if (ok && n > 0) tc_commit(o_final);
+      if (ok && n > 0) tc_commit_warp(o_final);
       // all MMAs of this CTA complete before TMEM is released
-      tc_commit(fin_bar);
+      tc_commit_warp(fin_bar);
       mbar_wait_drain(fin_bar, 0, a.wd);
     }
   } else {

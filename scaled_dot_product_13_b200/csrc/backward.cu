@@ -40,21 +40,21 @@ sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *o
   const size_t slabs = (size_t)pb.B * pb.Hkv;
   if (pl.path == SDPA_BWD_PATH_TC) {
     const DimPair dp = kDimPairs[pl.pair];
-    const int bn = bwd_tc_block(pl.pair);
-    if (128 % bn != 0) pl.rpad += 128;  // 96-row blocks end up to 95 rows behind the slab
+    const int bk = bwd_tc_key_block(dp.dqk, dp.dv), bq = kBwdTcQueryBlock;
+    if (128 % bk != 0) pl.rpad += 128;  // 48-row blocks end up to 47 rows behind the slab
     // Split a tile's block list where one tile would outlast the whole grid's
     // work spread over the SMs (few tiles with long lists: few query rows over
-    // many keys, or one KV head under many rows).  Work in block products: 4
-    // for a key tile's block, 3 for a query tile's.
+    // many keys, or one KV head under many rows).  Work in products per pair:
+    // 4 in a key tile, 3 in a query tile.
     const long long kt = (pb.S + 127) / 128, rt = (pl.rows + 127) / 128;
-    const long long kb = (pl.rows + bn - 1) / bn, rb = (pb.S + bn - 1) / bn;
-    const long long ideal = std::max<long long>(1, (long long)slabs * (kt * kb * 4 + rt * rb * 3) / sms);
-    auto parts = [&](long long blocks, int products) {
-      const long long want = (blocks * products + ideal - 1) / ideal;
+    const long long kb = (pl.rows + bk - 1) / bk, rb = (pb.S + bq - 1) / bq;
+    const long long ideal = std::max<long long>(1, (long long)slabs * (kt * kb * bk * 4 + rt * rb * bq * 3) / sms);
+    auto parts = [&](long long blocks, int block_products) {
+      const long long want = (blocks * block_products + ideal - 1) / ideal;
       return (int)std::max<long long>(1, std::min(want, blocks / kMinBlocksPerPart));
     };
-    pl.key_splits = parts(kb, 4);
-    pl.row_splits = parts(rb, 3);
+    pl.key_splits = parts(kb, 4 * bk);
+    pl.row_splits = parts(rb, 3 * bq);
     if (pl.key_splits > 1) {
       pl.key_part1_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dqk * sizeof(float));
       pl.key_part2_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dv * sizeof(float));

@@ -16,22 +16,33 @@
 // time.
 //
 // Warp roles (10 warps):
-//   0-7  softmax: warps w and w + 4 share TMEM lanes 32 (w % 4) .. +31 and take
-//        one half of a block's columns each.  Phase E: P = 2^(S c + nlse);
-//        phase F: dS = P (dP + ndelta) gain, with P kept in registers.  A half
-//        writes its packed values over its own columns only, so the two warps
-//        of a lane need no exchange.
+//   0-7  softmax.  Phase E: P = 2^(S c + nlse); phase F: dS = P (dP + ndelta) gain,
+//        with P kept in registers.  With two score buffers (ST = 2) warps 0-3
+//        take the even blocks and 4-7 the odd ones, a row per thread; with one,
+//        warps w and w + 4 share TMEM lanes 32 (w % 4) .. +31 and take one half of
+//        a block's columns each, packed over their own half only, so that the
+//        two need no exchange.
 //   8    TMA producer (X once, then Y1 and Y2 blocks through two rings, the row
 //        terms of a query block with its Y1)
 //   9    MMA issuer (the whole warp, one elected lane), in the order
-//            out2_j, S_{j+1}   after P_j   (runs under phase F of block j)
-//            out1_j, dP_{j+1}  after dS_j  (runs under phase E of block j+1)
-//        so the tensor pipe works on one pair while the softmax warps work on
-//        the other, with one S and one dP buffer: one thread's MMAs run in
-//        issue order, so S_{j+1} may overwrite P_j once out2_j is issued.
+//            out2_n, S_{n+ST}   after P_n
+//            out1_n, dP_{n+ST}  after dS_n
+//        One warp's MMAs run in issue order, so S_{n+ST} may overwrite P_n once
+//        out2_n is issued.
 //
-// TMEM (512 columns): S [0, BN), dP [BN, 2 BN), out1 [2 BN, ..), out2 behind.
-// Head dims 256 leave no room for dK and dV together: those take a CTA each.
+// What bounds it.  P_n -> out2_n, S_{n+1} -> P_{n+1} is a chain through one score
+// buffer: with ST = 1 it took 4300 cycles per 128 x 128 pairs of a key tile at
+// every head dim (E 1900 until the slower of an SM sub-partition's two warps is
+// through, then the two products and their hand-overs), against 2048 of tensor
+// work at head dim 128.  Two buffers of 64 columns let one warp group's
+// chain run under the other's.  Their cost is operand traffic: a 128 x 64 x 16
+// product with both operands in shared memory reads 6 KB (48 cycles) for 32
+// cycles of math.  So X, constant over a tile, is copied to TMEM where columns
+// are left and read from there (2 KB, 16 cycles).
+//
+// TMEM (512 columns): ST stages of S and dP, out1, out2, X1, X2 where they fit:
+// BwdTcRoles below lists what each head-dim pair takes.  Head dims from 192/192
+// leave no room for dK and dV together: those take a CTA each.
 #pragma once
 
 #include <type_traits>
@@ -50,41 +61,56 @@ constexpr int kBwdTcRows = 128;
 constexpr int kBwdTcSoftmaxWarps = 8;
 constexpr int kBwdTcThreads = (kBwdTcSoftmaxWarps + 2) * 32;
 
-// One kind of tile.  N1 / N2: ring slots of Y1 and Y2.
-template <int D1_, int D2_, int BN_, int N1_, int N2_, bool KEYS_, bool OUT1_, bool OUT2_>
+// One kind of tile.  ST: score buffers; N1 / N2: ring slots of Y1 and Y2;
+// XT1 / XT2: X1 / X2 are read from TMEM; ALIAS: X1 passes through the last Y1
+// slots on its way there.
+template <int D1_, int D2_, int BN_, int ST_, int N1_, int N2_, bool KEYS_, bool OUT1_, bool OUT2_, bool XT1_, bool XT2_,
+          bool ALIAS_ = false>
 struct BwdTcRole {
-  static constexpr int D1 = D1_, D2 = D2_, BN = BN_, N1 = N1_, N2 = N2_;
-  static constexpr bool KEYS = KEYS_, OUT1 = OUT1_, OUT2 = OUT2_;
+  static constexpr int D1 = D1_, D2 = D2_, BN = BN_, ST = ST_, N1 = N1_, N2 = N2_;
+  static constexpr bool KEYS = KEYS_, OUT1 = OUT1_, OUT2 = OUT2_, XT1 = XT1_, XT2 = XT2_, ALIAS = ALIAS_;
   static constexpr int kBoxes1 = (D1 + 63) / 64, kBoxes2 = (D2 + 63) / 64;
   static constexpr uint32_t kX1Bytes = kBoxes1 * 128 * 128;
   static constexpr uint32_t kX2Bytes = OUT1 ? kBoxes2 * 128 * 128 : 0;  // dP only
   static constexpr uint32_t kY1Bytes = kBoxes1 * BN * 128;
   static constexpr uint32_t kY2Bytes = kBoxes2 * BN * 128;
-  static constexpr uint32_t kX2Off = kX1Bytes;
+  static constexpr int kAliasSlots = ALIAS ? (kX1Bytes + kY1Bytes - 1) / kY1Bytes : 0;
+  static constexpr uint32_t kX2Off = ALIAS ? 0 : kX1Bytes;
   static constexpr uint32_t kY1Off = kX2Off + kX2Bytes;
+  static constexpr uint32_t kX1Off = ALIAS ? kY1Off + (N1 - kAliasSlots) * kY1Bytes : 0;
   static constexpr uint32_t kY2Off = kY1Off + N1 * kY1Bytes;
   static constexpr uint32_t kTermOff = kY2Off + N2 * kY2Bytes;  // [N1][2][BN] row terms
   static constexpr uint32_t kTermBytes = KEYS ? N1 * 2 * BN * 4 : 0;
   static constexpr uint32_t kBarOff = kTermOff + kTermBytes;
-  static constexpr int kNumBars = 2 * N1 + 2 * N2 + 7;
+  static constexpr int kNumBars = 2 * N1 + 2 * N2 + 4 * ST + 4;
   static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 16;
-  static constexpr int kOut1Col = OUT1 ? 2 * BN : BN;  // without out1 there is no dP
+  static constexpr int kStageCols = OUT1 ? 2 * BN : BN;  // S and dP of one stage
+  static constexpr int kOut1Col = ST * kStageCols;
   static constexpr int kOut2Col = kOut1Col + (OUT1 ? D1 : 0);
-  static constexpr int kH = BN / 2;  // columns per softmax thread
-  // staging of the finished tile: out1 in X1's memory; out2 in X2's, or in X1's
-  // where it is the only output
+  static constexpr int kX1Col = kOut2Col + (OUT2 ? D2 : 0);
+  static constexpr int kX2Col = kX1Col + (XT1 ? D1 / 2 : 0);
+  static constexpr int kColsUsed = kX2Col + (XT2 ? D2 / 2 : 0);
+  static constexpr int kParts = ST == 1 ? 2 : 1;  // softmax warps sharing a row
+  static constexpr int kH = BN / kParts;          // columns per softmax thread
+  // the finished tile is staged in the X tiles' memory: out1 where X1 was (X2
+  // where that is ring slots now), out2 where X2 was (X1 as the only output)
+  static constexpr uint32_t kStage1Off = 0;
   static constexpr uint32_t kStage2Off = OUT1 ? kX2Off : 0;
   static_assert(OUT1 || OUT2, "");
   static_assert(KEYS || (OUT1 && !OUT2), "query tiles give dQ");
-  static_assert(kOut2Col + (OUT2 ? D2 : 0) <= 512, "TMEM columns");
-  static_assert(N1 >= 2 || !OUT1, "Y1_j is held while S_{j+1} needs the next");
+  static_assert(ST == 1 || ST == 2, "");
+  static_assert(kColsUsed <= 512, "TMEM columns");
+  // Y1_n is held until out1_n, which is issued after S_{n+ST}
+  static_assert(N1 >= (OUT1 ? ST + 1 : ST) && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
+  static_assert(!ALIAS || (XT1 && OUT1 && !OUT2 && kX2Bytes >= kX1Bytes && N1 > kAliasSlots), "");
   static_assert(OUT1 || kBoxes2 <= kBoxes1, "out2's staging");
+  static_assert(!XT2 || OUT1, "");
   static_assert(kH % 16 == 0 && BN % 16 == 0, "");
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct BwdTcMaps {
-  CUtensorMap kx, vx, qy, doy;  // key tiles: X boxes of 128 rows, Y boxes of BN rows
+  CUtensorMap kx, vx, qy, doy;  // key tiles: X boxes of 128 rows, Y boxes of the kind's BN
   CUtensorMap qx, dox, ky, vy;  // query tiles
   CUtensorMap dq, dk, dv;       // 128-row boxes
 };
@@ -106,73 +132,63 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // The blocks of BN Y rows that a tile visits, in rising order.  Query tiles
 // see one range of keys.  Key tiles see, of each head's L packed rows, the same
-// range of queries [i_lo, i_hi); a block may span two heads.
+// range of queries [i_lo, i_hi); a block may span several heads.
+template <class Role>
 struct BwdBlocks {
-  bool keys;
-  int bn, first, end;        // block range
-  int L, R, i_lo, i_hi;
+  int end;        // blocks end here
+  int L, R;
+  int lo, hi;     // packed rows of the current head that the tile sees
+  int base;       // first packed row of that head
+  bool all;       // every row is visible: nothing to skip
 
-  // smallest visited block >= b, or -1
-  __device__ __forceinline__ int at_or_after(int b) const {
+  // Smallest visited block >= b (rising from call to call), or -1.  Leaves the
+  // first head with visible rows at or behind the block's first row as the
+  // current one.
+  __device__ __forceinline__ int at_or_after(int b) {
     if (b >= end) return -1;
-    if (!keys || i_hi - i_lo == L) return b;
-    for (;;) {
-      const int r0 = b * bn;
-      if (r0 >= R) return -1;
-      const int j = r0 / L;
-      int lo = j * L + i_lo;
-      if (r0 >= j * L + i_hi) lo += L;  // behind this head's visible rows
-      if (lo >= R) return -1;
-      if (r0 + bn > lo) return b;
-      b = lo / bn;
+    if constexpr (Role::KEYS) {
+      const int r0 = b * Role::BN;
+      while (r0 >= hi) {
+        lo += L;
+        hi += L;
+        base += L;
+        if (lo >= R) return -1;
+      }
+      if (!all && r0 + Role::BN <= lo) b = lo / Role::BN;
     }
+    return b;
+  }
+
+  // Query index of packed row r0 (the first of the last returned block).
+  __device__ __forceinline__ int query(int r0) const {
+    return r0 >= base ? r0 - base : r0 - base + L;
   }
 };
 
 template <class Role>
-__device__ __forceinline__ BwdBlocks bwd_blocks(const AttnParams &a, int x0) {
-  BwdBlocks w;
-  w.keys = Role::KEYS;
-  w.bn = Role::BN;
+__device__ __forceinline__ BwdBlocks<Role> bwd_blocks(const AttnParams &a, int x0, int &first) {
+  BwdBlocks<Role> w;
   w.L = a.L;
   w.R = a.R;
-  w.i_lo = 0;
-  w.i_hi = a.L;
-  w.first = 0;
+  w.base = 0;
+  w.lo = 0;
+  w.hi = a.L;
+  first = 0;
   if constexpr (Role::KEYS) {
     const int key_max = min(x0 + kBwdTcRows, a.S) - 1;
-    if (a.causal) w.i_lo = min(max(x0 - a.off, 0), a.L);
-    if (a.window > 0) w.i_hi = (int)max(0LL, min((long long)a.L, (long long)key_max + a.window - a.off));
-    w.end = w.i_lo < w.i_hi ? (a.R + Role::BN - 1) / Role::BN : 0;
+    if (a.causal) w.lo = min(max(x0 - a.off, 0), a.L);
+    if (a.window > 0) w.hi = (int)max(0LL, min((long long)a.L, (long long)key_max + a.window - a.off));
+    w.end = w.lo < w.hi ? (a.R + Role::BN - 1) / Role::BN : 0;
   } else {
     int pos_min, pos_max;
     packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
     const int kend = a.causal ? min(a.S, pos_max + 1) : a.S;
     const int kbeg = a.window > 0 ? max(0, pos_min - a.window + 1) : 0;
-    w.first = kbeg / Role::BN;
-    w.end = kend > kbeg ? (kend + Role::BN - 1) / Role::BN : w.first;
+    first = kbeg / Role::BN;
+    w.end = kend > kbeg ? (kend + Role::BN - 1) / Role::BN : first;
   }
+  w.all = w.hi - w.lo == a.L;
   return w;
-}
-
-// Does any pair of the tile and the block need its own mask test?  (Rows past
-// the slab have nlse = -inf, keys past S only matter as Y: their dS would meet
-// zero-filled rows, but P of a zero score may overflow.)
-template <class Role>
-__device__ __forceinline__ bool bwd_needs_mask(const AttnParams &a, int x0, int blk) {
-  int pos_min, pos_max, key_min, key_max;
-  if constexpr (Role::KEYS) {
-    const int r0 = blk * Role::BN;
-    packed_positions(a, r0, min(Role::BN, a.R - r0), pos_min, pos_max);
-    key_min = x0;
-    key_max = min(x0 + kBwdTcRows, a.S) - 1;
-  } else {
-    packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
-    key_min = blk * Role::BN;
-    key_max = key_min + Role::BN - 1;
-    if (key_max >= a.S) return true;
-  }
-  return (a.causal && key_max > pos_min) || (a.window > 0 && pos_max - key_min >= a.window);
 }
 
 // N consecutive TMEM columns of this thread's lane (N a multiple of 16).
@@ -188,31 +204,56 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, float *v) {
   }
 }
 
+// X (boxes of 128 rows x 64 columns, 128-byte swizzled) to TMEM as the A operand of
+// a first product: 16-bit pairs, a row per lane.  Four warps, one row per thread.
+template <int D>
+__device__ __forceinline__ void bwd_x_to_tmem(const uint8_t *x, uint32_t taddr, int r) {
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int chunk = c * 2 + i;
+      const uint4 t = *reinterpret_cast<const uint4 *>(x + (chunk >> 3) * (128 * 128) + sw128_offset(r, chunk & 7));
+      v[4 * i] = t.x;
+      v[4 * i + 1] = t.y;
+      v[4 * i + 2] = t.z;
+      v[4 * i + 3] = t.w;
+    }
+    tmem_st_u8x(taddr + c * 8, v);
+  }
+  tmem_wait_st();
+}
+
 template <bool kBF16, class Role>
 __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMap *tm_x1,
                                             const CUtensorMap *tm_x2, const CUtensorMap *tm_y1,
                                             const CUtensorMap *tm_y2, const CUtensorMap *tm_o1,
                                             const CUtensorMap *tm_o2, const BwdTcSpan &span, int id,
                                             uint8_t *smem) {
-  constexpr int BN = Role::BN, N1 = Role::N1, N2 = Role::N2, kH = Role::kH;
+  constexpr int BN = Role::BN, ST = Role::ST, N1 = Role::N1, N2 = Role::N2, kH = Role::kH;
   constexpr bool OUT1 = Role::OUT1, OUT2 = Role::OUT2, KEYS = Role::KEYS;
   const AttnParams &a = p.a;
-  uint8_t *sX1 = smem, *sX2 = smem + Role::kX2Off;
+  uint8_t *sX1 = smem + Role::kX1Off, *sX2 = smem + Role::kX2Off;
   uint8_t *sY1 = smem + Role::kY1Off, *sY2 = smem + Role::kY2Off;
   float *terms = reinterpret_cast<float *>(smem + Role::kTermOff);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Role::kBarOff);
   uint64_t *y1_full = bars, *y1_empty = y1_full + N1;
   uint64_t *y2_full = y1_empty + N1, *y2_empty = y2_full + N2;
-  uint64_t *x_full = y2_empty + N2;
-  uint64_t *s_full = x_full + 1;    // S_j complete (MMA -> softmax)
-  uint64_t *p_full = s_full + 1;    // P_j in TMEM, or S_j read (softmax -> MMA)
-  uint64_t *dp_full = p_full + 1;   // dP_j complete
-  uint64_t *ds_full = dp_full + 1;  // dS_j in TMEM
-  uint64_t *o_final = ds_full + 1;  // every product has completed
+  uint64_t *s_full = y2_empty + N2;  // [ST] S_n complete (MMA -> softmax)
+  uint64_t *p_full = s_full + ST;    // [ST] P_n in TMEM, or S_n read (softmax -> MMA)
+  uint64_t *dp_full = p_full + ST;   // [ST] dP_n complete
+  uint64_t *ds_full = dp_full + ST;  // [ST] dS_n in TMEM
+  uint64_t *x_full = ds_full + ST;
+  uint64_t *xt_full = x_full + 1;   // X copied to TMEM
+  uint64_t *o_final = xt_full + 1;  // every product has completed
   uint64_t *fin_bar = o_final + 1;  // teardown drain of the MMA warp
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin_bar + 1);
   constexpr int kProducerWarp = kBwdTcSoftmaxWarps, kMmaWarp = kBwdTcSoftmaxWarps + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool XT = Role::XT1 || Role::XT2;
+  // (through a shuffle, so that the compiler knows the roles' branches to be
+  // warp-uniform and keeps the MMA operands in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // --- work item: tile fastest (a slab's Y blocks stay in L2 while its tiles
   // run), then split, then slab; the tiles that visit most blocks first ---
@@ -232,11 +273,14 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       mbar_init(&y2_full[s], 1);
       mbar_init(&y2_empty[s], 1);
     }
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], kBwdTcSoftmaxWarps / ST);
+      mbar_init(&dp_full[s], 1);
+      mbar_init(&ds_full[s], kBwdTcSoftmaxWarps / ST);
+    }
     mbar_init(x_full, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kBwdTcSoftmaxWarps);
-    mbar_init(dp_full, 1);
-    mbar_init(ds_full, kBwdTcSoftmaxWarps);
+    mbar_init(xt_full, 4 * ((Role::XT1 ? 1 : 0) + (Role::XT2 ? 1 : 0)) + (XT ? 0 : 1));
     mbar_init(o_final, 1);
     mbar_init(fin_bar, 1);
     fence_barrier_init();
@@ -248,21 +292,25 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // launched as a programmatic dependent of the row-term kernel: nothing below
   // touches global memory before that grid has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the block list of this CTA: [begin, ...) of `count` visited blocks
-  const BwdBlocks walk = bwd_blocks<Role>(a, x0);
-  int begin = walk.at_or_after(walk.first), count = 0x7fffffff;
+  // the block list of this CTA: `count` visited blocks from `begin`
+  int begin, count = 0x7fffffff;
+  BwdBlocks<Role> walk = bwd_blocks<Role>(a, x0, begin);
   if (span.splits > 1) {
+    BwdBlocks<Role> w = walk;
     int total = 0;
-    for (int b = begin; b >= 0; b = walk.at_or_after(b + 1)) ++total;
+    for (int b = w.at_or_after(begin); b >= 0; b = w.at_or_after(b + 1)) ++total;
     const int per = (total + span.splits - 1) / span.splits;
     count = min(per, total - split * per);
+    begin = walk.at_or_after(begin);
     for (int s = 0; s < split * per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
     if (count <= 0) begin = -1;
+  } else {
+    begin = walk.at_or_after(begin);
   }
 
   if (warp == kProducerWarp) {
@@ -286,6 +334,8 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       int n = 0;
       for (int b = begin; b >= 0 && n < count; b = walk.at_or_after(b + 1), ++n) {
         const int s1 = n % N1, s2 = n % N2;
+        if (Role::ALIAS && n == N1 - Role::kAliasSlots)  // X1 has left the slot
+          if (!mbar_wait(xt_full, 0, a.wd, kWdTmaEmpty)) break;
         if (!mbar_wait(&y1_empty[s1], ((uint32_t)(n / N1) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
         mbar_arrive_expect_tx(&y1_full[s1], Role::kY1Bytes + (KEYS ? 2 * BN * 4 : 0));
         uint8_t *d1 = sY1 + s1 * Role::kY1Bytes;
@@ -313,104 +363,117 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         mbar_wait_drain(&y2_full[v % N2], (uint32_t)(v / N2) & 1u, a.wd);
     }
   } else if (warp == kMmaWarp) {
-    // ============================ MMA issuer ============================
-    // the whole warp, converged: see tc_mma_ss_warp
-    {
-      constexpr uint32_t kIdescS = umma_idesc_f16(kBF16, 128, BN, false, false);
-      constexpr uint32_t kIdesc1 = umma_idesc_f16(kBF16, 128, Role::D1, false, true);
-      constexpr uint32_t kIdesc2 = umma_idesc_f16(kBF16, 128, Role::D2, false, true);
-      const uint32_t x1 = smem_u32(sX1), x2 = smem_u32(sX2), y1 = smem_u32(sY1), y2 = smem_u32(sY2);
-      auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t code) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wd, code));
-      };
-      bool ok = wait(x_full, 0, kWdTmaFull);
-      // first products: 128 x BN scores over the head dim, both K-major
-      auto first = [&](uint32_t x, uint32_t y, int steps, uint32_t col) {
-        tc_fence_after();
-        const uint64_t a0 = umma_desc_sw128(x, 16, 1024);
-        const uint64_t b0 = umma_desc_sw128(y, 16, 1024);
+    // ========== MMA issuer: the whole warp, converged (see elect_leader) ==========
+    const uint32_t leader = elect_leader();
+    constexpr uint32_t kIdescS = umma_idesc_f16(kBF16, 128, BN, false, false);
+    constexpr uint32_t kIdesc1 = umma_idesc_f16(kBF16, 128, Role::D1, false, true);
+    constexpr uint32_t kIdesc2 = umma_idesc_f16(kBF16, 128, Role::D2, false, true);
+    const uint32_t x1 = smem_u32(sX1), x2 = smem_u32(sX2), y1 = smem_u32(sY1), y2 = smem_u32(sY2);
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t code) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wd, code));
+    };
+    // first products: 128 x BN scores over the head dim; Y K-major, X K-major in
+    // shared memory or in TMEM
+    auto first = [&](auto in_tmem, auto dim, uint32_t x, uint32_t y, uint32_t col) {
+      tc_fence_after();
+      const uint64_t a0 = umma_desc_sw128(x, 16, 1024);
+      const uint64_t b0 = umma_desc_sw128(y, 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < steps; ++ks)
-          tc_mma_ss_warp(tmem + col, umma_desc_advance(a0, (ks >> 2) * (128 * 128) + (ks & 3) * 32),
-                    umma_desc_advance(b0, (ks >> 2) * (BN * 128) + (ks & 3) * 32), kIdescS,
-                    ks > 0 ? 1u : 0u);
-      };
-      // second products: weights from TMEM (each half of the columns packed at
-      // the start of its own half) times the same Y block, MN-major
-      auto second = [&](uint32_t wcol, uint32_t y, uint32_t out, uint32_t idesc, bool fresh) {
-        tc_fence_after();
-        const uint64_t b0 = umma_desc_sw128_mn(y, BN * 128, 1024);
+      for (int ks = 0; ks < decltype(dim)::value / 16; ++ks) {
+        const uint64_t bd = umma_desc_advance(b0, (ks >> 2) * (BN * 128) + (ks & 3) * 32);
+        if constexpr (decltype(in_tmem)::value)
+          tc_mma_ts_warp(leader, tmem + col, tmem + x + ks * 8, bd, kIdescS, ks > 0 ? 1u : 0u);
+        else
+          tc_mma_ss_warp(leader, tmem + col, umma_desc_advance(a0, (ks >> 2) * (128 * 128) + (ks & 3) * 32), bd, kIdescS,
+                         ks > 0 ? 1u : 0u);
+      }
+    };
+    // second products: weights from TMEM (each part of the columns packed at the
+    // start of its own columns) times the same Y block, MN-major
+    auto second = [&](uint32_t wcol, uint32_t y, uint32_t out, uint32_t idesc, bool fresh) {
+      tc_fence_after();
+      const uint64_t b0 = umma_desc_sw128_mn(y, BN * 128, 1024);
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks) {
-          const int half = ks / (kH / 16);
-          tc_mma_ts_warp(tmem + out, tmem + wcol + half * kH + (ks - half * (kH / 16)) * 8,
-                    umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 ? 0u : 1u);
-        }
-      };
-      auto issue_s = [&](int n) -> bool {
-        const int s1 = n % N1;
-        if (!wait(&y1_full[s1], (uint32_t)(n / N1) & 1u, kWdTmaFull)) return false;
-        first(x1, y1 + s1 * Role::kY1Bytes, Role::D1 / 16, 0);
-        tc_commit_warp(s_full);
-        return true;
-      };
-      auto issue_dp = [&](int n) -> bool {
-        const int s2 = n % N2;
-        if (!wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull)) return false;
-        first(x2, y2 + s2 * Role::kY2Bytes, Role::D2 / 16, BN);
-        tc_commit_warp(dp_full);
-        if constexpr (!OUT2) tc_commit_warp(&y2_empty[s2]);
-        return true;
-      };
-      int n = 0;
-      int b = begin;
-      if (ok && b >= 0) {
-        ok = issue_s(0);
-        if constexpr (OUT1) ok = ok && issue_dp(0);
+      for (int ks = 0; ks < BN / 16; ++ks) {
+        const int part = ks / (kH / 16);
+        tc_mma_ts_warp(leader, tmem + out, tmem + wcol + part * kH + (ks - part * (kH / 16)) * 8,
+                       umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 ? 0u : 1u);
       }
-      while (ok && b >= 0 && n < count) {
-        b = walk.at_or_after(b + 1);
-        const bool more = b >= 0 && n + 1 < count;
-        const int s1 = n % N1, s2 = n % N2;
-        if (!(ok = wait(p_full, (uint32_t)n & 1u, kWdSoftmax))) break;
-        if constexpr (OUT2) {
-          if constexpr (!OUT1)
-            if (!(ok = wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull))) break;
-          second(0, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
-          tc_commit_warp(&y2_empty[s2]);
-          // (not after S_j: the softmax warps read the row terms of the slot)
-          if constexpr (!OUT1) tc_commit_warp(&y1_empty[s1]);
-        }
-        if (more && !(ok = issue_s(n + 1))) break;
-        if constexpr (OUT1) {
-          if (!(ok = wait(ds_full, (uint32_t)n & 1u, kWdSoftmax))) break;
-          second(BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
-          tc_commit_warp(&y1_empty[s1]);
-          if (more && !(ok = issue_dp(n + 1))) break;
-        }
-        ++n;
-        if (!more) break;
-      }
-      if (ok && n > 0) tc_commit_warp(o_final);
-      // all MMAs of this CTA complete before TMEM is released
-      tc_commit_warp(fin_bar);
-      mbar_wait_drain(fin_bar, 0, a.wd);
+    };
+    auto issue_s = [&](int n) -> bool {
+      const int s1 = n % N1, st = n % ST;
+      if (!wait(&y1_full[s1], (uint32_t)(n / N1) & 1u, kWdTmaFull)) return false;
+      first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
+            y1 + s1 * Role::kY1Bytes, st * Role::kStageCols);
+      tc_commit_warp(leader, &s_full[st]);
+      return true;
+    };
+    auto issue_dp = [&](int n) -> bool {
+      const int s2 = n % N2, st = n % ST;
+      if (!wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull)) return false;
+      first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
+            y2 + s2 * Role::kY2Bytes, st * Role::kStageCols + BN);
+      tc_commit_warp(leader, &dp_full[st]);
+      if constexpr (!OUT2) tc_commit_warp(leader, &y2_empty[s2]);
+      return true;
+    };
+    bool ok = wait(x_full, 0, kWdTmaFull);
+    if (XT) ok = ok && wait(xt_full, 0, kWdSoftmax);
+    // `issued` blocks have their first products under way, ST ahead of block n
+    int issued = 0, b = begin;
+    auto next = [&]() {
+      ++issued;
+      b = b >= 0 && issued < count ? walk.at_or_after(b + 1) : -1;
+    };
+    for (int i = 0; i < ST && ok && b >= 0; ++i) {
+      ok = issue_s(i);
+      if constexpr (OUT1) ok = ok && issue_dp(i);
+      next();
     }
+    int n = 0;
+    for (; ok && n < issued; ++n) {
+      const int s1 = n % N1, s2 = n % N2, st = n % ST;
+      const uint32_t ph = (uint32_t)(n / ST) & 1u;
+      const bool more = b >= 0;  // block n + ST
+      if (more) next();
+      if (!(ok = wait(&p_full[st], ph, kWdSoftmax))) break;
+      if constexpr (OUT2) {
+        if constexpr (!OUT1)
+          if (!(ok = wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull))) break;
+        second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
+        tc_commit_warp(leader, &y2_empty[s2]);
+        // (not after S_n: the softmax warps read the row terms of the slot)
+        if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[s1]);
+      }
+      if (more && !(ok = issue_s(n + ST))) break;
+      if constexpr (OUT1) {
+        if (!(ok = wait(&ds_full[st], ph, kWdSoftmax))) break;
+        second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
+        tc_commit_warp(leader, &y1_empty[s1]);
+        if (more && !(ok = issue_dp(n + ST))) break;
+      }
+    }
+    if (ok && n > 0) tc_commit_warp(leader, o_final);
+    // all MMAs of this CTA complete before TMEM is released
+    tc_commit_warp(leader, fin_bar);
+    mbar_wait_drain(fin_bar, 0, a.wd);
   } else {
-    // ===== softmax warps: X rows 32 (w % 4) .. +31, block columns half w / 4 =====
-    const int quarter = warp & 3, half = warp >> 2;
-    const int r = quarter * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    // ============ softmax warps: X rows 32 (w % 4) .. +31 ============
+    const int group = warp >> 2;
+    const int part = Role::kParts == 2 ? group : 0;  // columns [part kH, +kH) of every block
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = a.scale_log2;
     const float gain = bwd_gain<kBF16>(p, bh);
+    // query tiles: this row's terms and position, and the tile's positions
     float x_nlse = 0.f, x_ndelta = 0.f;
-    int pos = 0;  // query tiles: this row's position
+    int pos = 0, pos_min = 0, pos_max = 0;
     if constexpr (!KEYS) {
       x_nlse = p.nlse[(long long)bh * p.rpad + x0 + r];  // x0 + 127 < rpad
       x_ndelta = p.ndelta[(long long)bh * p.rpad + x0 + r];
       pos = (x0 + r) % a.L + a.off;
+      packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
     }
-    bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
       bool w = true;
       if (lane == 0) w = mbar_wait(bar, parity, a.wd, kWdMma);
@@ -423,20 +486,53 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
+    bool ok = true;
+    if constexpr (XT) {
+      ok = wait(x_full, 0);
+      if (Role::XT1 && group == 0) {
+        if (ok) bwd_x_to_tmem<Role::D1>(sX1, lanes + Role::kX1Col, r);
+        arrive(xt_full);
+      }
+      if (Role::XT2 && group == 1) {
+        if (ok) bwd_x_to_tmem<Role::D2>(sX2, lanes + Role::kX2Col, r);
+        arrive(xt_full);
+      }
+    }
     int n = 0;
-    for (int b = begin; b >= 0 && n < count; b = walk.at_or_after(b + 1), ++n) {
-      const float *t_nlse = terms + (n % N1) * 2 * BN + half * kH;
+    for (int b = begin; ok && b >= 0 && n < count; b = walk.at_or_after(b + 1), ++n) {
+      const int st = n % ST;
+      if (ST == 2 && st != group) continue;
+      const uint32_t ph = (uint32_t)(n / ST) & 1u;
+      const uint32_t t_s = lanes + st * Role::kStageCols + part * kH, t_dp = t_s + BN;
+      const float *t_nlse = terms + (n % N1) * 2 * BN + part * kH;
       const float *t_ndelta = t_nlse + BN;
-      if (!(ok = wait(s_full, (uint32_t)n & 1u))) break;
-      // the row terms came with Y1 (already complete: S_j was computed from it)
+      // Does any pair of the tile and the block need its own mask test?  (Rows
+      // past the slab have nlse = -inf; keys past S matter as Y only: their dS
+      // would meet zero-filled rows, but P of a zero score may overflow.)
+      bool masked = false;
+      int col_query = 0;  // key tiles: query index of this thread's first column
+      if constexpr (KEYS) {
+        if (a.causal) {
+          const int i0 = walk.query(b * BN);
+          const bool wraps = i0 + BN > a.L;
+          const int qmin = (wraps ? 0 : i0) + a.off, qmax = (wraps ? a.L : i0 + BN) - 1 + a.off;
+          masked = min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window);
+          col_query = i0 + part * kH;
+          if (col_query >= a.L) col_query %= a.L;
+        }
+      } else {
+        const int k0 = b * BN;
+        masked = k0 + BN > a.S || (a.causal && k0 + BN - 1 > pos_min) || (a.window > 0 && pos_max - k0 >= a.window);
+      }
+      if (!(ok = wait(&s_full[st], ph))) break;
+      // the row terms came with Y1 (already complete: S_n was computed from it)
       if constexpr (KEYS)
         if (!(ok = wait(&y1_full[n % N1], (uint32_t)(n / N1) & 1u))) break;
       // ---- phase E ----
       float w[kH];
-      tmem_ldn<kH>(tmem + lane_base + half * kH, w);
+      tmem_ldn<kH>(t_s, w);
       tmem_wait_ld();
-      if constexpr (!OUT2) arrive(p_full);  // S_j is free
-      const bool masked = bwd_needs_mask<Role>(a, x0, b);
+      if constexpr (!OUT2) arrive(&p_full[st]);  // S_n is free
       const float2 c2 = make_float2(c, c);
 #pragma unroll
       for (int i = 0; i < kH; i += 4) {
@@ -461,7 +557,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         if constexpr (KEYS) {
           const int key = x0 + r;
           const unsigned lim = a.window > 0 ? (unsigned)a.window : 0x80000000u;
-          int i = (b * BN + half * kH) % a.L;
+          int i = col_query;
 #pragma unroll
           for (int e = 0; e < kH; ++e) {
             if ((unsigned)(i + a.off - key) >= lim) {
@@ -471,7 +567,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
             if (++i == a.L) i = 0;
           }
         } else {
-          const VisibleRange vis = visible_range(a, pos, b * BN + half * kH);
+          const VisibleRange vis = visible_range(a, pos, b * BN + part * kH);
 #pragma unroll
           for (int e = 0; e < kH; ++e)
             if (!vis(e)) {
@@ -481,43 +577,45 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         }
       }
       if constexpr (OUT2) {
-        uint32_t pk[kH / 2];
 #pragma unroll
-        for (int i = 0; i < kH / 2; ++i) pk[i] = pack2<kBF16>(w[2 * i], w[2 * i + 1]);
+        for (int i = 0; i < kH; i += 16) {
+          uint32_t pk[8];
 #pragma unroll
-        for (int i = 0; i < kH / 2; i += 8) tmem_st_u8x(tmem + lane_base + half * kH + i, pk + i);
+          for (int e = 0; e < 8; ++e) pk[e] = pack2<kBF16>(w[i + 2 * e], w[i + 2 * e + 1]);
+          tmem_st_u8x(t_s + i / 2, pk);
+        }
         tmem_wait_st();
-        arrive(p_full);
+        arrive(&p_full[st]);
       }
       // ---- phase F ----
       if constexpr (OUT1) {
-        if (!(ok = wait(dp_full, (uint32_t)n & 1u))) break;
+        if (!(ok = wait(&dp_full[st], ph))) break;
+        float d[kH];
+        tmem_ldn<kH>(t_dp, d);
+        tmem_wait_ld();
         // two copies: a masked pair's dP may be anything, also not a number
         auto phase_f = [&](auto with_mask) {
 #pragma unroll
           for (int i0 = 0; i0 < kH; i0 += 16) {
-            float d[16];
-            tmem_ld16(tmem + lane_base + BN + half * kH + i0, d);
-            tmem_wait_ld();
             uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = i0; i < i0 + 16; i += 4) {
               float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
-              if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + i0 + i);
+              if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + i);
 #pragma unroll
               for (int e = 0; e < 4; e += 2) {
                 float2 t = add2(make_float2(d[i + e], d[i + e + 1]),
                                 e == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w));
                 if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
-                t = mul2(t, make_float2(w[i0 + i + e], w[i0 + i + e + 1]));
+                t = mul2(t, make_float2(w[i + e], w[i + e + 1]));
                 if constexpr (decltype(with_mask)::value) {
-                  if ((hidden >> (i0 + i + e)) & 1) t.x = 0.f;
-                  if ((hidden >> (i0 + i + e + 1)) & 1) t.y = 0.f;
+                  if ((hidden >> (i + e)) & 1) t.x = 0.f;
+                  if ((hidden >> (i + e + 1)) & 1) t.y = 0.f;
                 }
-                pk[(i + e) / 2] = pack2<kBF16>(t.x, t.y);
+                pk[(i - i0 + e) / 2] = pack2<kBF16>(t.x, t.y);
               }
             }
-            tmem_st_u8x(tmem + lane_base + BN + half * kH + i0 / 2, pk);
+            tmem_st_u8x(t_dp + i0 / 2, pk);
           }
         };
         if (masked)
@@ -525,7 +623,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         else
           phase_f(std::false_type());
         tmem_wait_st();
-        arrive(ds_full);
+        arrive(&ds_full[st]);
       }
     }
 
@@ -535,25 +633,25 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     ok = wait(have ? o_final : x_full, 0) && ok;
     const bool have_o = have && ok;
     const int nvalid = min(kBwdTcRows, xrows - x0);
-    auto finish = [&](int col, int d, float factor, uint8_t *stage, float *part) {
+    auto finish = [&](int col, int d, float factor, uint8_t *stage, float *out_part) {
       const int chunks = d / 16;
-      for (int c16 = half * chunks / 2; c16 < (half + 1) * chunks / 2; ++c16) {
+      for (int c16 = group * chunks / 2; c16 < (group + 1) * chunks / 2; ++c16) {
         float o[16];
         if (have_o) {
-          tmem_ld16(tmem + lane_base + col + c16 * 16, o);
+          tmem_ld16(lanes + col + c16 * 16, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = 0.f;
         }
-        if (part == nullptr) {
+        if (out_part == nullptr) {
           uint32_t w8[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w8[e] = pack2<kBF16>(o[2 * e] * factor, o[2 * e + 1] * factor);
           stage_16bit_x16(stage, r, c16, w8);
         } else if (r < nvalid) {  // fp32 sums, [split][slab][row][d]
           float4 *dst = reinterpret_cast<float4 *>(
-              part + ((((long long)split * a.B * a.Hkv + bh) * xrows + x0 + r) * d + c16 * 16));
+              out_part + ((((long long)split * a.B * a.Hkv + bh) * xrows + x0 + r) * d + c16 * 16));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -562,7 +660,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     };
     const bool split_out = span.splits > 1;
     if constexpr (OUT1)
-      finish(Role::kOut1Col, Role::D1, bwd_ds_factor<kBF16>(p, gain), sX1, split_out ? span.part1 : nullptr);
+      finish(Role::kOut1Col, Role::D1, bwd_ds_factor<kBF16>(p, gain), smem + Role::kStage1Off, split_out ? span.part1 : nullptr);
     if constexpr (OUT2)
       finish(Role::kOut2Col, Role::D2, bwd_dv_factor<kBF16>(), smem + Role::kStage2Off, split_out ? span.part2 : nullptr);
     if (!split_out) {
@@ -572,7 +670,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       if (warp == 0 && lane == 0) {
         if constexpr (OUT1)
           for (int bx = 0; bx < Role::kBoxes1 && bx * 64 < a.Dqk; ++bx)
-            tma_store_3d(tm_o1, sX1 + bx * (128 * 128), bx * 64, x0, bh);
+            tma_store_3d(tm_o1, smem + Role::kStage1Off + bx * (128 * 128), bx * 64, x0, bh);
         if constexpr (OUT2)
           for (int bx = 0; bx < Role::kBoxes2 && bx * 64 < a.Dv; ++bx)
             tma_store_3d(tm_o2, smem + Role::kStage2Off + bx * (128 * 128), bx * 64, x0, bh);
@@ -593,25 +691,51 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
 
 constexpr uint32_t bwd_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The kinds of tile of one head-dim pair, most work per block first.
+// The kinds of tile of one head-dim pair, most work per block first: TMEM columns
+//   pair      key tiles                          query tiles
+//   64/64     2 x 128 + 64 + 64  + X 32 + 32     2 x 128 + 64  + X 32 + 32
+//   80/80     2 x 128 + 80 + 80  + X 40 + 40     2 x 128 + 80  + X 40 + 40
+//   128/128   2 x 128 + 128 + 128                2 x 128 + 128 + X 64 + 64
+//   192/128   2 x  96 + 192 + 128                2 x 128 + 192 +   X2 64
+//   192/192   128 + 192 + X 96 + 96 (dK)         128 + 192 + X 96 + 96
+//             2 x  64 + 192 + X1 96 (dV)
+//   256/256   128 + 256 + X1 128    (dK)         128 + 256 + X1 128
+//             2 x  64 + 256 + X1 128 (dV)
 template <int DQK, int DV>
-struct BwdTcRoles {
-  // key tiles with dK and dV together: 128-row blocks where TMEM and shared
-  // memory have room, 96 or 64 otherwise
-  static constexpr int BN = DQK <= 128 ? 128 : DV <= 128 ? 96 : 64;
-  using Key = BwdTcRole<DQK, DV, BN, 2, 2, true, true, true>;
-  using Query = BwdTcRole<DQK, DV, BN, 2, 2, false, true, false>;
-  static constexpr int kKinds = 2;
+struct BwdTcRoles;
+template <int D>
+struct BwdTcRolesBoth {
+  using Key = BwdTcRole<D, D, 64, 2, 4, 4, true, true, true, D <= 80, D <= 80>;
+  using Query = BwdTcRole<D, D, 64, 2, 4, 4, false, true, false, true, true>;
+  using KeyV = void;
   // (more than half of an SM's, whatever the tiles need: a CTA takes all of TMEM)
   static constexpr uint32_t kSmem = bwd_max(120 * 1024, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
 };
 template <>
+struct BwdTcRoles<64, 64> : BwdTcRolesBoth<64> {};
+template <>
+struct BwdTcRoles<80, 80> : BwdTcRolesBoth<80> {};
+template <>
+struct BwdTcRoles<128, 128> : BwdTcRolesBoth<128> {};
+template <>
+struct BwdTcRoles<192, 128> {
+  using Key = BwdTcRole<192, 128, 48, 2, 4, 4, true, true, true, false, false>;
+  using Query = BwdTcRole<192, 128, 64, 2, 4, 3, false, true, false, false, true>;
+  using KeyV = void;
+  static constexpr uint32_t kSmem = bwd_max(Key::kSmemBytes, Query::kSmemBytes);
+};
+template <>
+struct BwdTcRoles<192, 192> {
+  using Key = BwdTcRole<192, 192, 64, 1, 3, 2, true, true, false, true, true>;
+  using Query = BwdTcRole<192, 192, 64, 1, 3, 2, false, true, false, true, true>;
+  using KeyV = BwdTcRole<192, 192, 64, 2, 3, 3, true, false, true, true, false>;
+  static constexpr uint32_t kSmem = bwd_max(KeyV::kSmemBytes, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
+};
+template <>
 struct BwdTcRoles<256, 256> {
-  using Key = BwdTcRole<256, 256, 64, 2, 1, true, true, false>;    // dK
-  using Query = BwdTcRole<256, 256, 64, 2, 1, false, true, false>;
-  using KeyV = BwdTcRole<256, 256, 64, 2, 2, true, false, true>;   // dV
-  static constexpr int BN = 64;
-  static constexpr int kKinds = 3;
+  using Key = BwdTcRole<256, 256, 64, 1, 3, 2, true, true, false, true, false, true>;
+  using Query = BwdTcRole<256, 256, 64, 1, 3, 2, false, true, false, true, false, true>;
+  using KeyV = BwdTcRole<256, 256, 64, 2, 3, 2, true, false, true, true, false>;
   static constexpr uint32_t kSmem = bwd_max(KeyV::kSmemBytes, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
 };
 
@@ -638,7 +762,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.qx, &tm.dox, &tm.ky, &tm.vy, &tm.dq, &tm.dq, rows, id, smem_raw);
     return;
   }
-  if constexpr (Roles::kKinds == 3) {
+  if constexpr (!std::is_void_v<typename Roles::KeyV>) {
     id -= row_ctas;
     bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
   }

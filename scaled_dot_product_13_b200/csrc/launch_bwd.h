@@ -40,9 +40,9 @@ sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err);
 sdpa_status launch_bwd_tile(const BwdLaunch &ln, std::string *err);
 sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err);
 
-// Y rows per block of the tcgen05 path's tiles (index into kDimPairs, up to 5).
-constexpr int bwd_tc_block(int pair) {
-  return kDimPairs[pair].dqk <= 128 ? 128 : kDimPairs[pair].dv <= 128 ? 96 : 64;
-}
+// Rows per block of the tcgen05 path: query rows of a key tile's block, keys of
+// a query tile's.
+constexpr int bwd_tc_key_block(int dqk, int dv) { return dqk == 192 && dv == 128 ? 48 : 64; }
+constexpr int kBwdTcQueryBlock = 64;
 
 }  // namespace sdpa

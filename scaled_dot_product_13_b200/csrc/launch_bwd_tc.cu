@@ -21,6 +21,10 @@ cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const float *part, voi
 template <bool kBF16, int DQK, int DV>
 sdpa_status run(const BwdLaunch &ln, std::string *err) {
   using Roles = BwdTcRoles<DQK, DV>;
+  static_assert(Roles::Key::BN == bwd_tc_key_block(DQK, DV) && Roles::Query::BN == kBwdTcQueryBlock,
+                "the plan counts the kernel's blocks");
+  if constexpr (!std::is_void_v<typename Roles::KeyV>)
+    static_assert(Roles::KeyV::BN == Roles::Key::BN, "both read the same boxes of Q and dO");
   auto kern = bwd_tc_kernel<kBF16, DQK, DV>;
   sdpa_status st = prepare_kernel((const void *)kern, kBwdTcThreads, Roles::kSmem, "bwd_tc_kernel", err);
   if (st != SDPA_OK) return st;
@@ -33,7 +37,7 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
                     pl.key_splits > 1 ? ln.key_part2 : nullptr};
   BwdTcSpan rows = {(pl.rows + 127) / 128, pl.row_splits, pl.row_splits > 1 ? ln.row_part : nullptr, nullptr};
   const long long key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
-  const long long ctas = key_ctas * (Roles::kKinds - 1) + row_ctas;
+  const long long ctas = key_ctas * (std::is_void_v<typename Roles::KeyV> ? 1 : 2) + row_ctas;
   const long long join_ctas = slabs * (pb.S > pl.rows ? (long long)pb.S : pl.rows) * 64 / 256;
   if (ctas > 0x7fffffffLL || join_ctas > 0x7fffffffLL) {
     *err = "problem needs more than 2^31 CTAs";
@@ -45,13 +49,13 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
     const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
     return encode_tma(m, pb.dtype, 3, base, dims, strides, box, err);
   };
-  constexpr int BN = Roles::BN;
+  constexpr int BK = Roles::Key::BN, BQ = Roles::Query::BN;
   const int R = pl.rows, S = pb.S, Dqk = pb.Dqk, Dv = pb.Dv;
   BwdTcMaps tm;
   if (!map(&tm.kx, ln.k, Dqk, S, 128) || !map(&tm.vx, ln.v, Dv, S, 128) ||
-      !map(&tm.qy, ln.q, Dqk, R, BN) || !map(&tm.doy, ln.dout, Dv, R, BN) ||
+      !map(&tm.qy, ln.q, Dqk, R, BK) || !map(&tm.doy, ln.dout, Dv, R, BK) ||
       !map(&tm.qx, ln.q, Dqk, R, 128) || !map(&tm.dox, ln.dout, Dv, R, 128) ||
-      !map(&tm.ky, ln.k, Dqk, S, BN) || !map(&tm.vy, ln.v, Dv, S, BN) ||
+      !map(&tm.ky, ln.k, Dqk, S, BQ) || !map(&tm.vy, ln.v, Dv, S, BQ) ||
       !map(&tm.dq, ln.dq, Dqk, R, 128) || !map(&tm.dk, ln.dk, Dqk, S, 128) ||
       !map(&tm.dv, ln.dv, Dv, S, 128))
     return SDPA_ERR_CUDA;
@@ -83,9 +87,6 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
 
 template <bool kBF16>
 sdpa_status run_dtype(const BwdLaunch &ln, std::string *err) {
-  static_assert(BwdTcRoles<128, 128>::BN == bwd_tc_block(2) && BwdTcRoles<192, 128>::BN == bwd_tc_block(3) &&
-                    BwdTcRoles<192, 192>::BN == bwd_tc_block(4) && BwdTcRoles<256, 256>::BN == bwd_tc_block(5),
-                "the plan's blocks are the kernel's");
   switch (ln.plan.pair) {
     case 0: return run<kBF16, 64, 64>(ln, err);
     case 1: return run<kBF16, 80, 80>(ln, err);

@@ -419,39 +419,41 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     };
     bool ok = wait(x_full, 0, kWdTmaFull);
     if (XT) ok = ok && wait(xt_full, 0, kWdSoftmax);
-    // `issued` blocks have their first products under way, ST ahead of block n
-    int issued = 0, b = begin;
-    auto next = [&]() {
-      ++issued;
-      b = b >= 0 && issued < count ? walk.at_or_after(b + 1) : -1;
-    };
-    for (int i = 0; i < ST && ok && b >= 0; ++i) {
-      ok = issue_s(i);
-      if constexpr (OUT1) ok = ok && issue_dp(i);
-      next();
-    }
-    int n = 0;
-    for (; ok && n < issued; ++n) {
-      const int s1 = n % N1, s2 = n % N2, st = n % ST;
-      const uint32_t ph = (uint32_t)(n / ST) & 1u;
-      const bool more = b >= 0;  // block n + ST
-      if (more) next();
-      if (!(ok = wait(&p_full[st], ph, kWdSoftmax))) break;
-      if constexpr (OUT2) {
-        if constexpr (!OUT1)
-          if (!(ok = wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull))) break;
-        second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
-        tc_commit_warp(leader, &y2_empty[s2]);
-        // (not after S_n: the softmax warps read the row terms of the slot)
-        if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[s1]);
+    // one loop, so that each product's code is there once: step n issues the
+    // second products of block n and the first ones of block n + ST
+    int issued = 0, b = begin, n = 0;
+    for (int m = -ST; ok; ++m) {
+      const bool have = m >= 0, more = b >= 0 && issued < count;  // blocks m, m + ST
+      if (have ? m >= issued : !more) {
+        if (have) break;
+        continue;  // fewer than ST blocks
       }
-      if (more && !(ok = issue_s(n + ST))) break;
+      const uint32_t um = (uint32_t)m;  // used from 0 on
+      const int s1 = um % N1, s2 = um % N2, st = um % ST;
+      const uint32_t ph = (um / ST) & 1u;
+      if (more) b = walk.at_or_after(b + 1);
+      if (have) {
+        if (!(ok = wait(&p_full[st], ph, kWdSoftmax))) break;
+        if constexpr (OUT2) {
+          if constexpr (!OUT1)
+            if (!(ok = wait(&y2_full[s2], (um / N2) & 1u, kWdTmaFull))) break;
+          second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, m == 0);
+          tc_commit_warp(leader, &y2_empty[s2]);
+          // (not after S_m: the softmax warps read the row terms of the slot)
+          if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[s1]);
+        }
+      }
+      if (more && !(ok = issue_s(m + ST))) break;
       if constexpr (OUT1) {
-        if (!(ok = wait(&ds_full[st], ph, kWdSoftmax))) break;
-        second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
-        tc_commit_warp(leader, &y1_empty[s1]);
-        if (more && !(ok = issue_dp(n + ST))) break;
+        if (have) {
+          if (!(ok = wait(&ds_full[st], ph, kWdSoftmax))) break;
+          second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, m == 0);
+          tc_commit_warp(leader, &y1_empty[s1]);
+        }
+        if (more && !(ok = issue_dp(m + ST))) break;
       }
+      if (more) ++issued;
+      if (have) ++n;
     }
     if (ok && n > 0) tc_commit_warp(leader, o_final);
     // all MMAs of this CTA complete before TMEM is released
@@ -498,10 +500,18 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         arrive(xt_full);
       }
     }
-    int n = 0;
-    for (int b = begin; ok && b >= 0 && n < count; b = walk.at_or_after(b + 1), ++n) {
-      const int st = n % ST;
-      if (ST == 2 && st != group) continue;
+    // step over `k` blocks
+    int b = begin, n = 0;
+    auto advance = [&](int k) {
+#pragma unroll 1
+      for (; k > 0 && b >= 0; --k) {
+        b = walk.at_or_after(b + 1);
+        if (++n >= count) b = -1;
+      }
+    };
+    if (ST == 2 && group == 1) advance(1);
+    while (ok && b >= 0) {
+      const int st = ST == 2 ? group : 0;
       const uint32_t ph = (uint32_t)(n / ST) & 1u;
       const uint32_t t_s = lanes + st * Role::kStageCols + part * kH, t_dp = t_s + BN;
       const float *t_nlse = terms + (n % N1) * 2 * BN + part * kH;
@@ -510,24 +520,22 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       // past the slab have nlse = -inf; keys past S matter as Y only: their dS
       // would meet zero-filled rows, but P of a zero score may overflow.)
       bool masked = false;
-      int col_query = 0;  // key tiles: query index of this thread's first column
+      int i0 = 0;  // key tiles: query index of the block's first row
       if constexpr (KEYS) {
         if (a.causal) {
-          const int i0 = walk.query(b * BN);
+          i0 = walk.query(b * BN);
           const bool wraps = i0 + BN > a.L;
           const int qmin = (wraps ? 0 : i0) + a.off, qmax = (wraps ? a.L : i0 + BN) - 1 + a.off;
           masked = min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window);
-          col_query = i0 + part * kH;
-          if (col_query >= a.L) col_query %= a.L;
         }
       } else {
         const int k0 = b * BN;
         masked = k0 + BN > a.S || (a.causal && k0 + BN - 1 > pos_min) || (a.window > 0 && pos_max - k0 >= a.window);
       }
-      if (!(ok = wait(&s_full[st], ph))) break;
-      // the row terms came with Y1 (already complete: S_n was computed from it)
+      // the row terms came with Y1
       if constexpr (KEYS)
         if (!(ok = wait(&y1_full[n % N1], (uint32_t)(n / N1) & 1u))) break;
+      if (!(ok = wait(&s_full[st], ph))) break;
       // ---- phase E ----
       float w[kH];
       tmem_ldn<kH>(t_s, w);
@@ -552,29 +560,27 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           w[i + e + 1] = t.y;
         }
       }
-      uint64_t hidden = 0;  // masked columns of this thread
       if (masked) {
+        // visible columns of this thread as bits
+        uint64_t seen = 0;
+        auto see = [&](int from, int to) {  // columns [from, to)
+          from = max(from, 0);
+          to = min(to, kH);
+          if (to > from) seen |= (~0ull >> (64 - (to - from))) << from;
+        };
         if constexpr (KEYS) {
-          const int key = x0 + r;
-          const unsigned lim = a.window > 0 ? (unsigned)a.window : 0x80000000u;
-          int i = col_query;
-#pragma unroll
-          for (int e = 0; e < kH; ++e) {
-            if ((unsigned)(i + a.off - key) >= lim) {
-              hidden |= 1ull << e;
-              w[e] = 0.f;
-            }
-            if (++i == a.L) i = 0;
-          }
+          // one interval of queries per head that the block touches
+          const int q_lo = x0 + r - a.off;
+          const int q_hi = a.window > 0 ? (int)min((long long)a.L, (long long)q_lo + a.window) : a.L;
+#pragma unroll 1
+          for (int col = -i0 - part * kH; col < kH; col += a.L) see(col + max(q_lo, 0), col + q_hi);
         } else {
           const VisibleRange vis = visible_range(a, pos, b * BN + part * kH);
-#pragma unroll
-          for (int e = 0; e < kH; ++e)
-            if (!vis(e)) {
-              hidden |= 1ull << e;
-              w[e] = 0.f;
-            }
+          see(vis.first, (int)min((long long)kH, (long long)vis.first + vis.span));
         }
+#pragma unroll
+        for (int e = 0; e < kH; ++e)
+          if (!((seen >> e) & 1)) w[e] = 0.f;
       }
       if constexpr (OUT2) {
 #pragma unroll
@@ -593,42 +599,37 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         float d[kH];
         tmem_ldn<kH>(t_dp, d);
         tmem_wait_ld();
-        // two copies: a masked pair's dP may be anything, also not a number
-        auto phase_f = [&](auto with_mask) {
+        if (masked) {  // a masked pair's dP may be anything, also not a number
 #pragma unroll
-          for (int i0 = 0; i0 < kH; i0 += 16) {
-            uint32_t pk[8];
+          for (int e = 0; e < kH; ++e)
+            if (w[e] == 0.f) d[e] = 0.f;
+        }
 #pragma unroll
-            for (int i = i0; i < i0 + 16; i += 4) {
-              float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
-              if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + i);
+        for (int j = 0; j < kH; j += 16) {
+          uint32_t pk[8];
 #pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                float2 t = add2(make_float2(d[i + e], d[i + e + 1]),
-                                e == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w));
-                if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
-                t = mul2(t, make_float2(w[i + e], w[i + e + 1]));
-                if constexpr (decltype(with_mask)::value) {
-                  if ((hidden >> (i + e)) & 1) t.x = 0.f;
-                  if ((hidden >> (i + e + 1)) & 1) t.y = 0.f;
-                }
-                pk[(i - i0 + e) / 2] = pack2<kBF16>(t.x, t.y);
-              }
+          for (int i = j; i < j + 16; i += 4) {
+            float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
+            if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + i);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              float2 t = add2(make_float2(d[i + e], d[i + e + 1]),
+                              e == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w));
+              if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
+              t = mul2(t, make_float2(w[i + e], w[i + e + 1]));
+              pk[(i - j + e) / 2] = pack2<kBF16>(t.x, t.y);
             }
-            tmem_st_u8x(t_dp + i0 / 2, pk);
           }
-        };
-        if (masked)
-          phase_f(std::true_type());
-        else
-          phase_f(std::false_type());
+          tmem_st_u8x(t_dp + j / 2, pk);
+        }
         tmem_wait_st();
         arrive(&ds_full[st]);
       }
+      advance(ST);
     }
 
     // ------------------------------ epilogue ------------------------------
-    const bool have = ok && n > 0;
+    const bool have = ok && begin >= 0;
     // (without a block, X may still be landing where the zeros are staged)
     ok = wait(have ? o_final : x_full, 0) && ok;
     const bool have_o = have && ok;

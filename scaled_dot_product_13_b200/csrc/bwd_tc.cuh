@@ -22,8 +22,11 @@
 //        warps w and w + 4 share TMEM lanes 32 (w % 4) .. +31 and take one half of
 //        a block's columns each, packed over their own half only, so that the
 //        two need no exchange.
-//   8    TMA producer (X once, then Y1 and Y2 blocks through two rings, the row
-//        terms of a query block with its Y1)
+//   8    TMA producer: X once, then Y1 and Y2 blocks through two rings, the row
+//        terms of a query block with its Y1.  It alone walks over the block list
+//        and tells the others with each Y1 slot which block it holds and whether
+//        the block needs its mask tested (a taken branch costs a warp about 25
+//        cycles: walking took the softmax warps 400 to 700 cycles a block)
 //   9    MMA issuer (the whole warp, one elected lane), in the order
 //            out2_n, S_{n+ST}   after P_n
 //            out1_n, dP_{n+ST}  after dS_n
@@ -81,7 +84,8 @@ struct BwdTcRole {
   static constexpr uint32_t kY2Off = kY1Off + N1 * kY1Bytes;
   static constexpr uint32_t kTermOff = kY2Off + N2 * kY2Bytes;  // [N1][2][BN] row terms
   static constexpr uint32_t kTermBytes = KEYS ? N1 * 2 * BN * 4 : 0;
-  static constexpr uint32_t kBarOff = kTermOff + kTermBytes;
+  static constexpr uint32_t kInfoOff = kTermOff + kTermBytes;   // [N1] BwdBlockInfo
+  static constexpr uint32_t kBarOff = kInfoOff + N1 * 16;
   static constexpr int kNumBars = 2 * N1 + 2 * N2 + 4 * ST + 4;
   static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 16;
   static constexpr int kStageCols = OUT1 ? 2 * BN : BN;  // S and dP of one stage
@@ -101,7 +105,7 @@ struct BwdTcRole {
   static_assert(ST == 1 || ST == 2, "");
   static_assert(kColsUsed <= 512, "TMEM columns");
   // Y1_n is held until out1_n, which is issued after S_{n+ST}
-  static_assert(N1 >= (OUT1 ? ST + 1 : ST) && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
+  static_assert(N1 >= ST + 1 && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
   static_assert(!ALIAS || (XT1 && OUT1 && !OUT2 && kX2Bytes >= kX1Bytes && N1 > kAliasSlots), "");
   static_assert(OUT1 || kBoxes2 <= kBoxes1, "out2's staging");
   static_assert(!XT2 || OUT1, "");
@@ -129,6 +133,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+
+// What the producer says about the block in a Y1 slot.
+struct __align__(16) BwdBlockInfo {
+  int row0;    // first Y row (behind the last block: the number of blocks)
+  int query0;  // key tiles: query index of packed row row0
+  int masked;  // some pair of tile and block needs its own test
+  int valid;   // 0 behind the last block
+};
 
 // The blocks of BN Y rows that a tile visits, in rising order.  Query tiles
 // see one range of keys.  Key tiles see, of each head's L packed rows, the same
@@ -237,6 +249,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   uint8_t *sX1 = smem + Role::kX1Off, *sX2 = smem + Role::kX2Off;
   uint8_t *sY1 = smem + Role::kY1Off, *sY2 = smem + Role::kY2Off;
   float *terms = reinterpret_cast<float *>(smem + Role::kTermOff);
+  BwdBlockInfo *info = reinterpret_cast<BwdBlockInfo *>(smem + Role::kInfoOff);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Role::kBarOff);
   uint64_t *y1_full = bars, *y1_empty = y1_full + N1;
   uint64_t *y2_full = y1_empty + N1, *y2_empty = y2_full + N2;
@@ -297,22 +310,6 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   // touches global memory before that grid has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the block list of this CTA: `count` visited blocks from `begin`
-  int begin, count = 0x7fffffff;
-  BwdBlocks<Role> walk = bwd_blocks<Role>(a, x0, begin);
-  if (span.splits > 1) {
-    BwdBlocks<Role> w = walk;
-    int total = 0;
-    for (int b = w.at_or_after(begin); b >= 0; b = w.at_or_after(b + 1)) ++total;
-    const int per = (total + span.splits - 1) / span.splits;
-    count = min(per, total - split * per);
-    begin = walk.at_or_after(begin);
-    for (int s = 0; s < split * per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
-    if (count <= 0) begin = -1;
-  } else {
-    begin = walk.at_or_after(begin);
-  }
-
   if (warp == kProducerWarp) {
     // ============================ TMA producer ============================
     if (lane == 0) {
@@ -330,34 +327,75 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       }
       const float *nlse = p.nlse + (long long)bh * p.rpad;
       const float *ndelta = p.ndelta + (long long)bh * p.rpad;
-      int u1 = 0, u2 = 0;
-      int n = 0;
-      for (int b = begin; b >= 0 && n < count; b = walk.at_or_after(b + 1), ++n) {
+      // the block list of this CTA: `count` visited blocks from `begin`
+      int begin, count = 0x7fffffff;
+      BwdBlocks<Role> walk = bwd_blocks<Role>(a, x0, begin);
+      if (span.splits > 1) {
+        BwdBlocks<Role> w = walk;
+        int total = 0;
+        for (int b = w.at_or_after(begin); b >= 0; b = w.at_or_after(b + 1)) ++total;
+        const int per = (total + span.splits - 1) / span.splits;
+        count = min(per, total - split * per);
+        begin = walk.at_or_after(begin);
+        for (int s = 0; s < split * per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
+        if (count <= 0) begin = -1;
+      } else {
+        begin = walk.at_or_after(begin);
+      }
+      int pos_min = 0, pos_max = 0;  // query tiles: the tile's positions
+      if constexpr (!KEYS) packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
+      int u1 = 0, u2 = 0, b = begin;
+      // behind the last block, one more slot per score buffer says so
+      int last = 0;
+      for (int n = 0; last < ST; ++n) {
         const int s1 = n % N1, s2 = n % N2;
         if (Role::ALIAS && n == N1 - Role::kAliasSlots)  // X1 has left the slot
           if (!mbar_wait(xt_full, 0, a.wd, kWdTmaEmpty)) break;
         if (!mbar_wait(&y1_empty[s1], ((uint32_t)(n / N1) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
+        BwdBlockInfo in = {u1, 0, 0, 0};
+        if (b < 0 || u1 >= count) {
+          info[s1] = in;
+          mbar_arrive(&y1_full[s1]);
+          ++last;
+          continue;
+        }
+        in.row0 = b * BN;
+        in.valid = 1;
+        // Does any pair of the tile and the block need its own mask test?  (Rows
+        // past the slab have nlse = -inf; keys past S matter as Y only: their dS
+        // would meet zero-filled rows, but P of a zero score may overflow.)
+        if constexpr (KEYS) {
+          in.query0 = walk.query(in.row0);
+          const bool wraps = in.query0 + BN > a.L;
+          const int qmin = (wraps ? 0 : in.query0) + a.off, qmax = (wraps ? a.L : in.query0 + BN) - 1 + a.off;
+          in.masked = a.causal && (min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window));
+        } else {
+          in.masked = in.row0 + BN > a.S || (a.causal && in.row0 + BN - 1 > pos_min) ||
+                      (a.window > 0 && pos_max - in.row0 >= a.window);
+        }
+        info[s1] = in;
         mbar_arrive_expect_tx(&y1_full[s1], Role::kY1Bytes + (KEYS ? 2 * BN * 4 : 0));
         uint8_t *d1 = sY1 + s1 * Role::kY1Bytes;
 #pragma unroll
         for (int bx = 0; bx < Role::kBoxes1; ++bx)
-          tma_load_3d(d1 + bx * (BN * 128), tm_y1, &y1_full[s1], bx * 64, b * BN, bh);
-        if constexpr (KEYS) {  // b BN + BN <= rpad
-          bulk_load(terms + s1 * 2 * BN, nlse + b * BN, BN * 4, &y1_full[s1]);
-          bulk_load(terms + s1 * 2 * BN + BN, ndelta + b * BN, BN * 4, &y1_full[s1]);
+          tma_load_3d(d1 + bx * (BN * 128), tm_y1, &y1_full[s1], bx * 64, in.row0, bh);
+        if constexpr (KEYS) {  // row0 + BN <= rpad
+          bulk_load(terms + s1 * 2 * BN, nlse + in.row0, BN * 4, &y1_full[s1]);
+          bulk_load(terms + s1 * 2 * BN + BN, ndelta + in.row0, BN * 4, &y1_full[s1]);
         }
         ++u1;
+        b = walk.at_or_after(b + 1);
         if (!mbar_wait(&y2_empty[s2], ((uint32_t)(n / N2) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
         mbar_arrive_expect_tx(&y2_full[s2], Role::kY2Bytes);
         uint8_t *d2 = sY2 + s2 * Role::kY2Bytes;
 #pragma unroll
         for (int bx = 0; bx < Role::kBoxes2; ++bx)
-          tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], bx * 64, b * BN, bh);
+          tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], bx * 64, in.row0, bh);
         ++u2;
       }
       // drain copies still landing (only ever waits after an abort)
       mbar_wait_drain(x_full, 0, a.wd);
-      for (int v = max(u1 - N1, 0); v < u1; ++v)
+      for (int v = max(u1 + last - N1, 0); v < u1; ++v)  // (not the slots used once more)
         mbar_wait_drain(&y1_full[v % N1], (uint32_t)(v / N1) & 1u, a.wd);
       for (int v = max(u2 - N2, 0); v < u2; ++v)
         mbar_wait_drain(&y2_full[v % N2], (uint32_t)(v / N2) & 1u, a.wd);
@@ -370,7 +408,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     constexpr uint32_t kIdesc2 = umma_idesc_f16(kBF16, 128, Role::D2, false, true);
     const uint32_t x1 = smem_u32(sX1), x2 = smem_u32(sX2), y1 = smem_u32(sY1), y2 = smem_u32(sY2);
     auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t code) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wd, code));
+      return mbar_wait_warp(bar, parity, a.wd, code);
     };
     // first products: 128 x BN scores over the head dim; Y K-major, X K-major in
     // shared memory or in TMEM
@@ -400,38 +438,21 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
                        umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 ? 0u : 1u);
       }
     };
-    auto issue_s = [&](int n) -> bool {
-      const int s1 = n % N1, st = n % ST;
-      if (!wait(&y1_full[s1], (uint32_t)(n / N1) & 1u, kWdTmaFull)) return false;
-      first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
-            y1 + s1 * Role::kY1Bytes, st * Role::kStageCols);
-      tc_commit_warp(leader, &s_full[st]);
-      return true;
-    };
-    auto issue_dp = [&](int n) -> bool {
-      const int s2 = n % N2, st = n % ST;
-      if (!wait(&y2_full[s2], (uint32_t)(n / N2) & 1u, kWdTmaFull)) return false;
-      first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
-            y2 + s2 * Role::kY2Bytes, st * Role::kStageCols + BN);
-      tc_commit_warp(leader, &dp_full[st]);
-      if constexpr (!OUT2) tc_commit_warp(leader, &y2_empty[s2]);
-      return true;
-    };
     bool ok = wait(x_full, 0, kWdTmaFull);
     if (XT) ok = ok && wait(xt_full, 0, kWdSoftmax);
-    // one loop, so that each product's code is there once: step n issues the
-    // second products of block n and the first ones of block n + ST
-    int issued = 0, b = begin, n = 0;
-    for (int m = -ST; ok; ++m) {
-      const bool have = m >= 0, more = b >= 0 && issued < count;  // blocks m, m + ST
-      if (have ? m >= issued : !more) {
-        if (have) break;
-        continue;  // fewer than ST blocks
-      }
-      const uint32_t um = (uint32_t)m;  // used from 0 on
-      const int s1 = um % N1, s2 = um % N2, st = um % ST;
+    // one loop, so that each product's code is there once: step m issues the
+    // second products of block m and the first ones of block m + ST
+    int issued = 0, n = 0;
+    bool more = true;
+    for (int m = -ST; ok && (m < 0 || m < issued); ++m) {
+      const uint32_t um = (uint32_t)m, un = (uint32_t)(m + ST);
+      const bool have = m >= 0;
+      const int s1 = um % N1, s2 = um % N2, st = un % ST, t1 = un % N1, t2 = un % N2;
       const uint32_t ph = (um / ST) & 1u;
-      if (more) b = walk.at_or_after(b + 1);
+      if (more) {
+        if (!(ok = wait(&y1_full[t1], (un / N1) & 1u, kWdTmaFull))) break;
+        more = __any_sync(0xffffffffu, info[t1].valid);
+      }
       if (have) {
         if (!(ok = wait(&p_full[st], ph, kWdSoftmax))) break;
         if constexpr (OUT2) {
@@ -443,16 +464,26 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[s1]);
         }
       }
-      if (more && !(ok = issue_s(m + ST))) break;
+      if (more) {
+        first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
+              y1 + t1 * Role::kY1Bytes, st * Role::kStageCols);
+        tc_commit_warp(leader, &s_full[st]);
+        ++issued;
+      }
       if constexpr (OUT1) {
         if (have) {
           if (!(ok = wait(&ds_full[st], ph, kWdSoftmax))) break;
           second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, m == 0);
           tc_commit_warp(leader, &y1_empty[s1]);
         }
-        if (more && !(ok = issue_dp(m + ST))) break;
+        if (more) {
+          if (!(ok = wait(&y2_full[t2], (un / N2) & 1u, kWdTmaFull))) break;
+          first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
+                y2 + t2 * Role::kY2Bytes, st * Role::kStageCols + BN);
+          tc_commit_warp(leader, &dp_full[st]);
+          if constexpr (!OUT2) tc_commit_warp(leader, &y2_empty[t2]);
+        }
       }
-      if (more) ++issued;
       if (have) ++n;
     }
     if (ok && n > 0) tc_commit_warp(leader, o_final);
@@ -467,19 +498,16 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = a.scale_log2;
     const float gain = bwd_gain<kBF16>(p, bh);
-    // query tiles: this row's terms and position, and the tile's positions
+    // query tiles: this row's terms and position
     float x_nlse = 0.f, x_ndelta = 0.f;
-    int pos = 0, pos_min = 0, pos_max = 0;
+    int pos = 0;
     if constexpr (!KEYS) {
       x_nlse = p.nlse[(long long)bh * p.rpad + x0 + r];  // x0 + 127 < rpad
       x_ndelta = p.ndelta[(long long)bh * p.rpad + x0 + r];
       pos = (x0 + r) % a.L + a.off;
-      packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
     }
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-      bool w = true;
-      if (lane == 0) w = mbar_wait(bar, parity, a.wd, kWdMma);
-      w = __shfl_sync(0xffffffffu, (int)w, 0) != 0;
+      const bool w = mbar_wait_warp(bar, parity, a.wd, kWdMma);
       tc_fence_after();
       return w;
     };
@@ -500,41 +528,25 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         arrive(xt_full);
       }
     }
-    // step over `k` blocks
-    int b = begin, n = 0;
-    auto advance = [&](int k) {
-#pragma unroll 1
-      for (; k > 0 && b >= 0; --k) {
-        b = walk.at_or_after(b + 1);
-        if (++n >= count) b = -1;
-      }
-    };
-    if (ST == 2 && group == 1) advance(1);
-    while (ok && b >= 0) {
-      const int st = ST == 2 ? group : 0;
-      const uint32_t ph = (uint32_t)(n / ST) & 1u;
-      const uint32_t t_s = lanes + st * Role::kStageCols + part * kH, t_dp = t_s + BN;
-      const float *t_nlse = terms + (n % N1) * 2 * BN + part * kH;
+    bool any = false;  // the tile has a block
+    for (uint32_t n = ST == 2 ? group : 0; ok; n += ST) {
+      constexpr int kStage = Role::kStageCols;
+      const uint32_t st = n % ST, ph = (n / ST) & 1u, slot = n % N1;
+      const uint32_t t_s = lanes + st * kStage + part * kH, t_dp = t_s + BN;
+      const float *t_nlse = terms + slot * 2 * BN + part * kH;
       const float *t_ndelta = t_nlse + BN;
-      // Does any pair of the tile and the block need its own mask test?  (Rows
-      // past the slab have nlse = -inf; keys past S matter as Y only: their dS
-      // would meet zero-filled rows, but P of a zero score may overflow.)
-      bool masked = false;
-      int i0 = 0;  // key tiles: query index of the block's first row
-      if constexpr (KEYS) {
-        if (a.causal) {
-          i0 = walk.query(b * BN);
-          const bool wraps = i0 + BN > a.L;
-          const int qmin = (wraps ? 0 : i0) + a.off, qmax = (wraps ? a.L : i0 + BN) - 1 + a.off;
-          masked = min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window);
-        }
-      } else {
-        const int k0 = b * BN;
-        masked = k0 + BN > a.S || (a.causal && k0 + BN - 1 > pos_min) || (a.window > 0 && pos_max - k0 >= a.window);
+      // what the block is, and (key tiles) the row terms came with Y1
+      if (!(ok = wait(&y1_full[slot], (n / N1) & 1u))) break;
+      const BwdBlockInfo in = info[slot];
+      if (!in.valid) {
+        any = in.row0 > 0;
+        break;
       }
-      // the row terms came with Y1
-      if constexpr (KEYS)
-        if (!(ok = wait(&y1_full[n % N1], (uint32_t)(n / N1) & 1u))) break;
+      float nl[KEYS ? kH : 1];
+      if constexpr (KEYS) {
+#pragma unroll
+        for (int i = 0; i < kH; i += 4) *reinterpret_cast<float4 *>(nl + i) = *reinterpret_cast<const float4 *>(t_nlse + i);
+      }
       if (!(ok = wait(&s_full[st], ph))) break;
       // ---- phase E ----
       float w[kH];
@@ -543,24 +555,19 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       if constexpr (!OUT2) arrive(&p_full[st]);  // S_n is free
       const float2 c2 = make_float2(c, c);
 #pragma unroll
-      for (int i = 0; i < kH; i += 4) {
-        float4 nl = make_float4(x_nlse, x_nlse, x_nlse, x_nlse);
-        if constexpr (KEYS) nl = *reinterpret_cast<const float4 *>(t_nlse + i);
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          float2 t = fma2(make_float2(w[i + e], w[i + e + 1]), c2,
-                          e == 0 ? make_float2(nl.x, nl.y) : make_float2(nl.z, nl.w));
-          if ((((i + e) >> 1) & 3) < SDPA_BWD_POLY_OF4) {
-            t = exp2_poly2(t);
-          } else {
-            t.x = fast_exp2(t.x);
-            t.y = fast_exp2(t.y);
-          }
-          w[i + e] = t.x;
-          w[i + e + 1] = t.y;
+      for (int i = 0; i < kH; i += 2) {
+        float2 t = fma2(make_float2(w[i], w[i + 1]), c2,
+                        KEYS ? make_float2(nl[KEYS ? i : 0], nl[KEYS ? i + 1 : 0]) : make_float2(x_nlse, x_nlse));
+        if (((i >> 1) & 3) < SDPA_BWD_POLY_OF4) {
+          t = exp2_poly2(t);
+        } else {
+          t.x = fast_exp2(t.x);
+          t.y = fast_exp2(t.y);
         }
+        w[i] = t.x;
+        w[i + 1] = t.y;
       }
-      if (masked) {
+      if (in.masked) {
         // visible columns of this thread as bits
         uint64_t seen = 0;
         auto see = [&](int from, int to) {  // columns [from, to)
@@ -573,9 +580,9 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           const int q_lo = x0 + r - a.off;
           const int q_hi = a.window > 0 ? (int)min((long long)a.L, (long long)q_lo + a.window) : a.L;
 #pragma unroll 1
-          for (int col = -i0 - part * kH; col < kH; col += a.L) see(col + max(q_lo, 0), col + q_hi);
+          for (int col = -in.query0 - part * kH; col < kH; col += a.L) see(col + max(q_lo, 0), col + q_hi);
         } else {
-          const VisibleRange vis = visible_range(a, pos, b * BN + part * kH);
+          const VisibleRange vis = visible_range(a, pos, in.row0 + part * kH);
           see(vis.first, (int)min((long long)kH, (long long)vis.first + vis.span));
         }
 #pragma unroll
@@ -599,7 +606,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         float d[kH];
         tmem_ldn<kH>(t_dp, d);
         tmem_wait_ld();
-        if (masked) {  // a masked pair's dP may be anything, also not a number
+        if (in.masked) {  // a masked pair's dP may be anything, also not a number
 #pragma unroll
           for (int e = 0; e < kH; ++e)
             if (w[e] == 0.f) d[e] = 0.f;
@@ -625,11 +632,10 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         tmem_wait_st();
         arrive(&ds_full[st]);
       }
-      advance(ST);
     }
 
     // ------------------------------ epilogue ------------------------------
-    const bool have = ok && begin >= 0;
+    const bool have = ok && any;
     // (without a block, X may still be landing where the zeros are staged)
     ok = wait(have ? o_final : x_full, 0) && ok;
     const bool have_o = have && ok;

@@ -115,6 +115,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
   }
 }
 
+// The same wait by a whole converged warp; the result is uniform.  The common
+// case (the phase has completed) is one try and one vote without a taken branch.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, const Watchdog &wd,
+                                               uint32_t code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, code));
+}
+
 // Teardown wait: only the time limit ends it (used to drain in-flight copies
 // before a CTA exits, even when the watchdog has already tripped).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t *bar, uint32_t parity,

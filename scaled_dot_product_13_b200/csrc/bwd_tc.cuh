@@ -82,10 +82,13 @@ struct BwdTcRole {
   static constexpr uint32_t kY1Off = kX2Off + kX2Bytes;
   static constexpr uint32_t kX1Off = ALIAS ? kY1Off + (N1 - kAliasSlots) * kY1Bytes : 0;
   static constexpr uint32_t kY2Off = kY1Off + N1 * kY1Bytes;
-  static constexpr uint32_t kTermOff = kY2Off + N2 * kY2Bytes;  // [N1][2][BN] row terms
-  static constexpr uint32_t kTermBytes = KEYS ? N1 * 2 * BN * 4 : 0;
-  static constexpr uint32_t kInfoOff = kTermOff + kTermBytes;   // [N1] BwdBlockInfo
-  static constexpr uint32_t kBarOff = kInfoOff + N1 * 16;
+  static constexpr uint32_t kTermOff = kY2Off + N2 * kY2Bytes;  // [NT][2][BN] row terms
+  // row terms and block notes: behind Y1's slot where that is held until the block
+  // is done, else (released after S_n) ST more, so that block n's stay until P_n
+  static constexpr int NT = OUT1 ? N1 : N1 + ST;
+  static constexpr uint32_t kTermBytes = KEYS ? NT * 2 * BN * 4 : 0;
+  static constexpr uint32_t kInfoOff = kTermOff + kTermBytes;  // [NT] BwdBlockInfo
+  static constexpr uint32_t kBarOff = kInfoOff + NT * 16;
   static constexpr int kNumBars = 2 * N1 + 2 * N2 + 4 * ST + 4;
   static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 16;
   static constexpr int kStageCols = OUT1 ? 2 * BN : BN;  // S and dP of one stage
@@ -104,7 +107,7 @@ struct BwdTcRole {
   static_assert(KEYS || (OUT1 && !OUT2), "query tiles give dQ");
   static_assert(ST == 1 || ST == 2, "");
   static_assert(kColsUsed <= 512, "TMEM columns");
-  // Y1_n is held until out1_n, which is issued after S_{n+ST}
+  // Y1_n is held until out1_n (without out1, until S_n), issued after S_{n+ST}
   static_assert(N1 >= ST + 1 && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
   static_assert(!ALIAS || (XT1 && OUT1 && !OUT2 && kX2Bytes >= kX1Bytes && N1 > kAliasSlots), "");
   static_assert(OUT1 || kBoxes2 <= kBoxes1, "out2's staging");
@@ -243,7 +246,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
                                             const CUtensorMap *tm_y2, const CUtensorMap *tm_o1,
                                             const CUtensorMap *tm_o2, const BwdTcSpan &span, int id,
                                             uint8_t *smem) {
-  constexpr int BN = Role::BN, ST = Role::ST, N1 = Role::N1, N2 = Role::N2, kH = Role::kH;
+  constexpr int BN = Role::BN, ST = Role::ST, N1 = Role::N1, N2 = Role::N2, NT = Role::NT, kH = Role::kH;
   constexpr bool OUT1 = Role::OUT1, OUT2 = Role::OUT2, KEYS = Role::KEYS;
   const AttnParams &a = p.a;
   uint8_t *sX1 = smem + Role::kX1Off, *sX2 = smem + Role::kX2Off;
@@ -348,13 +351,13 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       // behind the last block, one more slot per score buffer says so
       int last = 0;
       for (int n = 0; last < ST; ++n) {
-        const int s1 = n % N1, s2 = n % N2;
+        const int s1 = n % N1, s2 = n % N2, nt = n % NT;
         if (Role::ALIAS && n == N1 - Role::kAliasSlots)  // X1 has left the slot
           if (!mbar_wait(xt_full, 0, a.wd, kWdTmaEmpty)) break;
         if (!mbar_wait(&y1_empty[s1], ((uint32_t)(n / N1) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
         BwdBlockInfo in = {u1, 0, 0, 0};
         if (b < 0 || u1 >= count) {
-          info[s1] = in;
+          info[nt] = in;
           mbar_arrive(&y1_full[s1]);
           ++last;
           continue;
@@ -373,15 +376,15 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           in.masked = in.row0 + BN > a.S || (a.causal && in.row0 + BN - 1 > pos_min) ||
                       (a.window > 0 && pos_max - in.row0 >= a.window);
         }
-        info[s1] = in;
+        info[nt] = in;
         mbar_arrive_expect_tx(&y1_full[s1], Role::kY1Bytes + (KEYS ? 2 * BN * 4 : 0));
         uint8_t *d1 = sY1 + s1 * Role::kY1Bytes;
 #pragma unroll
         for (int bx = 0; bx < Role::kBoxes1; ++bx)
           tma_load_3d(d1 + bx * (BN * 128), tm_y1, &y1_full[s1], bx * 64, in.row0, bh);
         if constexpr (KEYS) {  // row0 + BN <= rpad
-          bulk_load(terms + s1 * 2 * BN, nlse + in.row0, BN * 4, &y1_full[s1]);
-          bulk_load(terms + s1 * 2 * BN + BN, ndelta + in.row0, BN * 4, &y1_full[s1]);
+          bulk_load(terms + nt * 2 * BN, nlse + in.row0, BN * 4, &y1_full[s1]);
+          bulk_load(terms + nt * 2 * BN + BN, ndelta + in.row0, BN * 4, &y1_full[s1]);
         }
         ++u1;
         b = walk.at_or_after(b + 1);
@@ -449,35 +452,41 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       const bool have = m >= 0;
       const int s1 = um % N1, s2 = um % N2, st = un % ST, t1 = un % N1, t2 = un % N2;
       const uint32_t ph = (um / ST) & 1u;
-      if (more) {
-        if (!(ok = wait(&y1_full[t1], (un / N1) & 1u, kWdTmaFull))) break;
-        more = __any_sync(0xffffffffu, info[t1].valid);
+      // Y1 of block m + ST, which is as a rule there long before P_m
+      if (have && more)
+        ok = mbar_wait_warp2(&p_full[st], ph, kWdSoftmax, &y1_full[t1], (un / N1) & 1u, kWdTmaFull, a.wd);
+      else if (have)
+        ok = wait(&p_full[st], ph, kWdSoftmax);
+      else if (more)
+        ok = wait(&y1_full[t1], (un / N1) & 1u, kWdTmaFull);
+      if (!ok) break;
+      if (OUT2 && have) {
+        if constexpr (!OUT1)
+          if (!(ok = wait(&y2_full[s2], (um / N2) & 1u, kWdTmaFull))) break;
+        second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, m == 0);
+        tc_commit_warp(leader, &y2_empty[s2]);
       }
-      if (have) {
-        if (!(ok = wait(&p_full[st], ph, kWdSoftmax))) break;
-        if constexpr (OUT2) {
-          if constexpr (!OUT1)
-            if (!(ok = wait(&y2_full[s2], (um / N2) & 1u, kWdTmaFull))) break;
-          second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, m == 0);
-          tc_commit_warp(leader, &y2_empty[s2]);
-          // (not after S_m: the softmax warps read the row terms of the slot)
-          if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[s1]);
-        }
-      }
+      if (more) more = __any_sync(0xffffffffu, info[un % NT].valid);
       if (more) {
         first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
               y1 + t1 * Role::kY1Bytes, st * Role::kStageCols);
         tc_commit_warp(leader, &s_full[st]);
+        if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[t1]);
         ++issued;
       }
       if constexpr (OUT1) {
+        if (have && more)
+          ok = mbar_wait_warp2(&ds_full[st], ph, kWdSoftmax, &y2_full[t2], (un / N2) & 1u, kWdTmaFull, a.wd);
+        else if (have)
+          ok = wait(&ds_full[st], ph, kWdSoftmax);
+        else if (more)
+          ok = wait(&y2_full[t2], (un / N2) & 1u, kWdTmaFull);
+        if (!ok) break;
         if (have) {
-          if (!(ok = wait(&ds_full[st], ph, kWdSoftmax))) break;
           second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, m == 0);
           tc_commit_warp(leader, &y1_empty[s1]);
         }
         if (more) {
-          if (!(ok = wait(&y2_full[t2], (un / N2) & 1u, kWdTmaFull))) break;
           first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
                 y2 + t2 * Role::kY2Bytes, st * Role::kStageCols + BN);
           tc_commit_warp(leader, &dp_full[st]);
@@ -531,13 +540,13 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     bool any = false;  // the tile has a block
     for (uint32_t n = ST == 2 ? group : 0; ok; n += ST) {
       constexpr int kStage = Role::kStageCols;
-      const uint32_t st = n % ST, ph = (n / ST) & 1u, slot = n % N1;
+      const uint32_t st = n % ST, ph = (n / ST) & 1u, slot = n % N1, nt = n % NT;
       const uint32_t t_s = lanes + st * kStage + part * kH, t_dp = t_s + BN;
-      const float *t_nlse = terms + slot * 2 * BN + part * kH;
+      const float *t_nlse = terms + nt * 2 * BN + part * kH;
       const float *t_ndelta = t_nlse + BN;
       // what the block is, and (key tiles) the row terms came with Y1
       if (!(ok = wait(&y1_full[slot], (n / N1) & 1u))) break;
-      const BwdBlockInfo in = info[slot];
+      const BwdBlockInfo in = info[nt];
       if (!in.valid) {
         any = in.row0 > 0;
         break;

@@ -123,6 +123,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, c
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, code));
 }
 
+// Both of two barriers: the two tries overlap (one satisfied wait costs 72
+// cycles, nearly all of it the try's latency).
+__device__ __forceinline__ bool mbar_wait_warp2(uint64_t *bar, uint32_t parity, uint32_t code,
+                                                uint64_t *bar2, uint32_t parity2, uint32_t code2,
+                                                const Watchdog &wd) {
+  const bool a = mbar_try_wait(smem_u32(bar), parity), b = mbar_try_wait(smem_u32(bar2), parity2);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, code) && mbar_wait(bar2, parity2, wd, code2));
+}
+
 // Teardown wait: only the time limit ends it (used to drain in-flight copies
 // before a CTA exits, even when the watchdog has already tripped).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t *bar, uint32_t parity,

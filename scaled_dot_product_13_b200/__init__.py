@@ -15,8 +15,10 @@ hq // (Hq // Hkv); query i sits at key position i + S - L.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 
 __all__ = ["forward", "forward_ws", "forward_noalloc", "forward_ex", "Options", "workspace_bytes", "plan", "device_status",
            "backward", "backward_workspace_bytes", "BackwardOptions", "BWD_PATH_AUTO", "BWD_PATH_TILE", "BWD_PATH_TC",
@@ -27,6 +29,7 @@ __all__ = ["forward", "forward_ws", "forward_noalloc", "forward_ex", "Options", 
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB: ctypes.CDLL | None = None
+_NOTHING = contextlib.nullcontext()
 
 PATH_AUTO, PATH_SPLITKV, PATH_TC, PATH_TC2, PATH_WIDE, PATH_TC_DUAL, PATH_TC_KSPLIT, PATH_TC2_LOOP = \
     0, 1, 2, 3, 4, 5, 6, 7
@@ -124,7 +127,7 @@ def load_library() -> ctypes.CDLL:
     lib.sdpa_backward_workspace_bytes.restype = sz
     ll = ctypes.c_longlong
     lib.sdpa_rotary_init.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(RotaryPlan)]
-    lib.sdpa_rotary.argtypes = [ctypes.POINTER(RotaryPlan), ctypes.POINTER(RotaryTensor), i, i, i, vp, i, ll, ll,
+    lib.sdpa_rotary.argtypes = [ctypes.POINTER(RotaryPlan), vp, i, i, i, vp, i, ll, ll,
                                 i, i, vp]
     lib.sdpa_device_status.argtypes = [i]
     lib.sdpa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -334,53 +337,57 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
     from the stream-ordered pool."""
     import torch
 
-    lib = load_library()
+    lib = _LIB or load_library()
     B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
-    sc = float(Dqk ** -0.5 if scale is None else scale)
     dt = _dtype_code(q)
-    for name, t in (("k", k), ("v", v)):
-        if t.device != q.device:
-            raise SdpaError(1, f"{name} must be on q's device")
+    dtype, device, f32 = q.dtype, q.device, torch.float32
+    if k.device != device or v.device != device:
+        raise SdpaError(1, "k and v must be on q's device")
+    rows = (B, Hq, L)
 
-    def want(name, t, shape, dtype):
-        if t is not None and not (t.device == q.device and t.dtype == dtype and t.is_contiguous()
-                                  and tuple(t.shape) == tuple(shape)):
-            raise SdpaError(1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on q's device")
+    def want(name, t, shape, kind):
+        if t.shape != shape or t.dtype != kind or t.device != device or not t.is_contiguous():
+            raise SdpaError(1, f"{name} must be a contiguous {kind} tensor of shape {tuple(shape)} on q's device")
+        return t.data_ptr()
 
-    for name, t in (("out", out), ("lse", lse), ("dout", dout)):
-        if t is None:
-            raise SdpaError(1, f"{name} is needed")
-    want("out", out, (B, Hq, L, Dv), q.dtype)
-    want("dout", dout, (B, Hq, L, Dv), q.dtype)
-    want("dq", dq, q.shape, q.dtype)
-    want("dk", dk, k.shape, q.dtype)
-    want("dv", dv, v.shape, q.dtype)
-    want("lse", lse, (B, Hq, L), torch.float32)
-    want("dlse", dlse, (B, Hq, L), torch.float32)
-    want("sinks", sinks, (Hq,), torch.float32)
-    want("dsinks", dsinks, (Hq,), torch.float32)
-    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
-        raise SdpaError(1, "workspace must be contiguous and on q's device")
+    if out is None or lse is None or dout is None:
+        raise SdpaError(1, "out, lse and dout are needed")
     opt = BackwardOptions()
     if q_offset is not None:
         opt.has_q_offset, opt.q_offset = 1, int(q_offset)
-    opt.sinks, opt.dsinks, opt.dlse = (t.data_ptr() if t is not None else None for t in (sinks, dsinks, dlse))
-    opt.force_path = int(force_path)
-    with torch.cuda.device(q.device):
+    if sinks is not None:
+        opt.sinks = want("sinks", sinks, (Hq,), f32)
+    if dsinks is not None:
+        opt.dsinks = want("dsinks", dsinks, (Hq,), f32)
+    if dlse is not None:
+        opt.dlse = want("dlse", dlse, rows, f32)
+    if force_path:
+        opt.force_path = int(force_path)
+    opt = ctypes.byref(opt)
+    causal, window_size = 1 if causal else 0, int(window_size)
+    with _on(device):
+        # (q, k and v are contiguous)
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
-        if workspace is None and stream is None:
-            n = lib.sdpa_backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, int(bool(causal)), int(window_size),
-                                                  dt, ctypes.byref(opt))
-            # invalid problems are left for the call to name
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-        ws_ptr = 0 if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib.sdpa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                 dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, L, S,
-                                 Dqk, Dv, sc, int(bool(causal)), int(window_size), dt, ctypes.byref(opt), ws_ptr,
-                                 ws_bytes, _call_stream(stream, q.device)))
+        ws_ptr = ws_bytes = 0
+        if workspace is not None:
+            if workspace.device != device or not workspace.is_contiguous():
+                raise SdpaError(1, "workspace must be contiguous and on q's device")
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif stream is None:
+            ws_bytes = lib.sdpa_backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, causal, window_size, dt, opt)
+            if ws_bytes:  # (invalid problems are left for the call to name)
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+                ws_ptr = workspace.data_ptr()
+        st = lib.sdpa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), want("out", out, rows + (Dv,), dtype),
+                               want("lse", lse, rows, f32), want("dout", dout, rows + (Dv,), dtype),
+                               want("dq", dq, q.shape, dtype), want("dk", dk, k.shape, dtype),
+                               want("dv", dv, v.shape, dtype), B, Hq, Hkv, L, S, Dqk, Dv,
+                               Dqk ** -0.5 if scale is None else scale, causal, window_size, dt, opt, ws_ptr, ws_bytes,
+                               _call_stream(stream, device))
+    if st:
+        _check(st)
     return dq, dk, dv
 
 
@@ -409,7 +416,16 @@ def _call_stream(stream, device):
     """The handle of ``stream``, by default the current stream of ``device``."""
     import torch
 
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on(device):
+    """``device`` as the current one for a call (nothing to do as a rule)."""
+    import torch
+
+    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def rotary(plan: RotaryPlan, q, k=None, positions=None, offset: int = 0, inverse: bool = False,
@@ -422,45 +438,62 @@ def rotary(plan: RotaryPlan, q, k=None, positions=None, offset: int = 0, inverse
     (the inputs themselves: in place); by default new dense [B, H, L, D]."""
     import torch
 
-    lib = load_library()
+    lib = _LIB or load_library()
     if not isinstance(plan, RotaryPlan):
         raise SdpaError(1, "plan must come from rotary_plan")
     if k is None and out_k is not None:
         raise SdpaError(1, "out_k without k")
-    pairs = [("q", q, out_q)] + ([("k", k, out_k)] if k is not None else [])
-    tensors, outs = (RotaryTensor * 2)(), []
-    for name, x, _ in pairs:
-        if x.dim() != 4 or x.shape[3] != plan.head_dim:
-            raise SdpaError(1, f"{name} must be [B, H, L, {plan.head_dim}] (got {tuple(x.shape)})")
-        if not x.is_cuda or x.device != q.device:
-            raise SdpaError(1, f"{name} must be a CUDA tensor, on q's device")
-        if x.dtype != q.dtype or (x.shape[0], x.shape[2]) != (q.shape[0], q.shape[2]):
-            raise SdpaError(1, "q and k must share dtype, batch and length")
-        if x.stride(3) != 1:
-            raise SdpaError(1, f"{name}'s last dim must be contiguous")
-    B, _, L, D = (int(n) for n in q.shape)
+    if q.dim() != 4 or not q.is_cuda:
+        raise SdpaError(1, f"q must be a CUDA tensor [B, H, L, {plan.head_dim}]")
+    B, Hq, L, D = q.shape
+    dtype, device = q.dtype, q.device
     dt = _dtype_code(q)
-    pos_ptr, bits, pos_stride = None, 0, 0
-    if positions is not None:
-        if positions.device != q.device or positions.dtype not in (torch.int32, torch.int64):
-            raise SdpaError(1, "positions must be an int32 or int64 tensor on q's device")
-        if tuple(positions.shape) not in ((L,), (1, L), (B, L)) or (L > 1 and positions.stride(-1) != 1):
-            raise SdpaError(1, f"positions must be [L], [1, L] or [B, L] with L = {L}, contiguous along L")
-        pos_ptr, bits = positions.data_ptr(), 32 if positions.dtype == torch.int32 else 64
-        if positions.dim() == 2 and positions.shape[0] == B and B > 1:
-            pos_stride = positions.stride(0)
-    with torch.cuda.device(q.device):
-        for n, (name, x, out) in enumerate(pairs):
-            if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or out.stride(3) != 1:
-                raise SdpaError(1, f"out_{name} must have {name}'s shape, dtype and device, its last dim contiguous")
-            tensors[n] = RotaryTensor(x.data_ptr(), out.data_ptr(), x.shape[1], Strides(*x.stride()[:3]),
-                                      Strides(*out.stride()[:3]))
-            outs.append(out)
-        _check(lib.sdpa_rotary(ctypes.byref(plan), tensors, len(pairs), B, L, pos_ptr, bits, pos_stride,
-                               int(offset), int(bool(inverse)), dt, _call_stream(stream, q.device)))
-    return outs[0] if k is None else tuple(outs)
+    with _on(device):
+        out_q, fields = _rotary_tensor("q", q, out_q, plan.head_dim, B, L, dtype, device)
+        if k is not None:
+            out_k, more = _rotary_tensor("k", k, out_k, plan.head_dim, B, L, dtype, device)
+            fields += more
+        pos_ptr, bits, pos_stride = None, 0, 0
+        if positions is not None:
+            if positions.device != device or positions.dtype not in (torch.int32, torch.int64):
+                raise SdpaError(1, "positions must be an int32 or int64 tensor on q's device")
+            shape = positions.shape
+            if not (len(shape) in (1, 2) and shape[-1] == L and (len(shape) == 1 or shape[0] in (1, B))) \
+                    or (L > 1 and positions.stride(-1) != 1):
+                raise SdpaError(1, f"positions must be [L], [1, L] or [B, L] with L = {L}, contiguous along L")
+            pos_ptr, bits = positions.data_ptr(), 32 if positions.dtype == torch.int32 else 64
+            if len(shape) == 2 and shape[0] == B and B > 1:
+                pos_stride = positions.stride(0)
+        count = len(fields) // 9
+        st = lib.sdpa_rotary(plan, struct.pack(_ROTARY_TENSOR * count, *fields), count, B, L, pos_ptr, bits, pos_stride,
+                             offset, 1 if inverse else 0, dt, _call_stream(stream, device))
+    if st:
+        _check(st)
+    return out_q if k is None else (out_q, out_k)
+
+
+# sdpa_rotary_tensor: x, out, heads, x's strides, out's strides
+_ROTARY_TENSOR = "QQi4xqqqqqq"
+
+
+def _rotary_tensor(name, x, out, D, B, L, dtype, device):
+    """The checked output of one tensor, and the fields of its sdpa_rotary_tensor."""
+    import torch
+
+    shape = x.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise SdpaError(1, f"{name} must be [B, H, L, {D}] (got {tuple(shape)})")
+    if x.device != device or x.dtype != dtype or shape[0] != B or shape[2] != L:
+        raise SdpaError(1, "q and k must share device, dtype, batch and length")
+    xb, xh, xt, xd = x.stride()
+    if xd != 1:
+        raise SdpaError(1, f"{name}'s last dim must be contiguous")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.shape != shape or out.dtype != dtype or out.device != device or out.stride(3) != 1:
+        raise SdpaError(1, f"out_{name} must have {name}'s shape, dtype and device, its last dim contiguous")
+    ob, oh, ot, _ = out.stride()
+    return out, (x.data_ptr(), out.data_ptr(), shape[1], xb, xh, xt, ob, oh, ot)
 
 
 def _num_sms() -> int:

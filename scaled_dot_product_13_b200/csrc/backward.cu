@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -18,6 +19,9 @@ sdpa_status refuse(sdpa_status st, const char *msg) { return set_error(st, msg);
 // Blocks each part of a split tile keeps at least: below that its operand
 // loads and its share of the join cost more than the parallelism gives.
 constexpr int kMinBlocksPerPart = 4;
+// ... and a list is only split when it is this much longer than an SM's share:
+// at 1.3 (the causal 192/128 case, a ragged chunk) splitting cost 6 to 18 %.
+constexpr double kSplitOver = 1.5;
 
 sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *out) {
   BwdPlan pl;
@@ -44,27 +48,43 @@ sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *o
     if (128 % bk != 0) pl.rpad += 128;  // 48-row blocks end up to 47 rows behind the slab
     // Split a tile's block list where one tile would outlast the whole grid's
     // work spread over the SMs (few tiles with long lists: few query rows over
-    // many keys, or one KV head under many rows).  Work in products per pair:
-    // 4 in a key tile, 3 in a query tile.
-    const long long kt = (pb.S + 127) / 128, rt = (pl.rows + 127) / 128;
-    const long long kb = (pl.rows + bk - 1) / bk, rb = (pb.S + bq - 1) / bq;
-    const long long ideal = std::max<long long>(1, (long long)slabs * (kt * kb * bk * 4 + rt * rb * bq * 3) / sms);
-    auto parts = [&](long long blocks, int block_products) {
-      const long long want = (blocks * block_products + ideal - 1) / ideal;
-      return (int)std::max<long long>(1, std::min(want, blocks / kMinBlocksPerPart));
+    // many keys, one KV head under many rows, the first keys of a causal call).
+    // Work in pairs of row and key that the mask leaves, times 4 products in a
+    // key tile, 3 in a query tile.
+    const int g = pb.Hq / pb.Hkv;
+    const double first = pb.causal ? std::min<double>(pb.S, pb.q_offset + 1.0) : pb.S;
+    const double last = pb.causal ? std::min<double>(pb.S, (double)pb.q_offset + pb.L) : pb.S;
+    double per_row = 0.5 * (first + last);  // keys that a row sees, on average
+    if (pb.window > 0) per_row = std::min<double>(per_row, pb.window);
+    const double ideal = (double)slabs * g * pb.L * per_row * 7 / sms;
+    // the longest lists: of the first keys, and of the last rows (whose tile
+    // spans all positions where it runs over the end of a head)
+    const long long seen_rows = pb.window > 0 ? std::min<long long>(pb.L, (long long)pb.window + 128) : pb.L;
+    const long long span = g > 1 && pb.L % 128 != 0 ? pb.L : std::min(pb.L, 128);
+    const long long row_keys = pb.window > 0 ? std::min<long long>(last, pb.window + span) : (long long)last;
+    const long long kb = (g * seen_rows + bk - 1) / bk, rb = (row_keys + bq - 1) / bq;
+    auto parts = [&](long long blocks, int pairs, int *per) {
+      const double over = (double)blocks * pairs * 128 / ideal;
+      int n = 1;
+      if (over > kSplitOver) n = (int)std::max(1.0, std::min(std::ceil(over), (double)(blocks / kMinBlocksPerPart)));
+      *per = (int)((blocks + n - 1) / n);
+      return n;
     };
-    pl.key_splits = parts(kb, 4 * bk);
-    pl.row_splits = parts(rb, 3 * bq);
+    pl.key_splits = parts(kb, 4 * bk, &pl.key_per);
+    pl.row_splits = parts(rb, 3 * bq, &pl.row_per);
+    pl.rows_first = (long long)pl.row_per * bq * 3 > (long long)pl.key_per * bk * 4;
     if (pl.key_splits > 1) {
       pl.key_part1_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dqk * sizeof(float));
       pl.key_part2_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dv * sizeof(float));
     }
     if (pl.row_splits > 1)
       pl.row_part_bytes = align256((size_t)pl.row_splits * slabs * pl.rows * dp.dqk * sizeof(float));
+    if (pl.key_splits > 1 || pl.row_splits > 1)
+      pl.count_bytes = align256(slabs * ((pb.S + 127) / 128 + (pl.rows + 127) / 128) * sizeof(int));
   }
   pl.row_bytes = align256(slabs * pl.rpad * sizeof(float));
   pl.norm_bytes = align256(slabs * 16);
-  pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes + pl.key_part1_bytes + pl.key_part2_bytes + pl.row_part_bytes;
+  pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes + pl.count_bytes + pl.key_part1_bytes + pl.key_part2_bytes + pl.row_part_bytes;
   *out = pl;
   return SDPA_OK;
 }
@@ -170,6 +190,9 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
   ln.ndelta = reinterpret_cast<float *>(ws + pl.row_bytes);
   ln.norms = reinterpret_cast<unsigned int *>(ws + 2 * pl.row_bytes);
   ws += 2 * pl.row_bytes + pl.norm_bytes;
+  ln.key_parts = reinterpret_cast<int *>(ws);
+  ln.row_parts = ln.key_parts + (size_t)B * Hkv * ((S + 127) / 128);
+  ws += pl.count_bytes;
   ln.key_part1 = reinterpret_cast<float *>(ws);
   ln.key_part2 = reinterpret_cast<float *>(ws + pl.key_part1_bytes);
   ln.row_part = reinterpret_cast<float *>(ws + pl.key_part1_bytes + pl.key_part2_bytes);

@@ -124,8 +124,11 @@ struct BwdTcMaps {
 
 // Tiles of one kind within the grid.
 struct BwdTcSpan {
-  int tiles, splits;  // per slab: row tiles, and parts of each tile's block list
-  float *part1, *part2;  // splits > 1: fp32 sums [split][slab][X rows][D]
+  int tiles;   // per slab
+  int splits;  // most parts that a block list is cut into, `per` blocks each
+  int per;
+  int *parts;            // splits > 1: [slab][tile] parts of each tile, and where that
+  float *part1, *part2;  // is above 1 their fp32 sums [split][slab][X rows][D]
 };
 
 // Untiled copy global -> shared (16-byte aligned, a multiple of 16 bytes).
@@ -140,7 +143,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // What the producer says about the block in a Y1 slot.
 struct __align__(16) BwdBlockInfo {
   int row0;    // first Y row (behind the last block: the number of blocks)
-  int query0;  // key tiles: query index of packed row row0
+  int query0;  // key tiles: query index of packed row row0 (behind the last: the tile's parts)
   int masked;  // some pair of tile and block needs its own test
   int valid;   // 0 behind the last block
 };
@@ -271,12 +274,23 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   // warp-uniform and keeps the MMA operands in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-  // --- work item: tile fastest (a slab's Y blocks stay in L2 while its tiles
-  // run), then split, then slab; the tiles that visit most blocks first ---
-  int tile = id % span.tiles;
-  id /= span.tiles;
-  const int split = id % span.splits, bh = id / span.splits;
-  if (!KEYS) tile = span.tiles - 1 - tile;
+  // --- work item.  Key tiles: tile fastest (a slab's query blocks stay in L2
+  // while its tiles run), then split, then slab.  Query tiles, which run last and
+  // read the smaller K and V: slab fastest, so that the grid ends with the tiles
+  // of fewest blocks.  The tiles that visit most blocks come first in both ---
+  int tile, split, bh;
+  if (KEYS) {
+    tile = id % span.tiles;
+    id /= span.tiles;
+    split = id % span.splits;
+    bh = id / span.splits;
+  } else {
+    const int slabs = a.B * a.Hkv;
+    bh = id % slabs;
+    id /= slabs;
+    split = id % span.splits;
+    tile = span.tiles - 1 - id / span.splits;
+  }
   const int x0 = tile * kBwdTcRows;
   const int xrows = KEYS ? a.S : a.R;
 
@@ -331,70 +345,94 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       const float *nlse = p.nlse + (long long)bh * p.rpad;
       const float *ndelta = p.ndelta + (long long)bh * p.rpad;
       // the block list of this CTA: `count` visited blocks from `begin`
-      int begin, count = 0x7fffffff;
+      int begin, count = 0x7fffffff, parts = 1;
       BwdBlocks<Role> walk = bwd_blocks<Role>(a, x0, begin);
       if (span.splits > 1) {
         BwdBlocks<Role> w = walk;
         int total = 0;
         for (int b = w.at_or_after(begin); b >= 0; b = w.at_or_after(b + 1)) ++total;
-        const int per = (total + span.splits - 1) / span.splits;
-        count = min(per, total - split * per);
+        // (the last part takes what an estimate of `per` may have left)
+        parts = min(span.splits, max(1, (total + span.per - 1) / span.per));
+        count = total - split * span.per;
+        if (split < span.splits - 1) count = min(span.per, count);
         begin = walk.at_or_after(begin);
-        for (int s = 0; s < split * per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
-        if (count <= 0) begin = -1;
+        for (int s = 0; s < split * span.per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
+        if (split == 0) span.parts[bh * span.tiles + tile] = parts;
       } else {
         begin = walk.at_or_after(begin);
       }
       int pos_min = 0, pos_max = 0;  // query tiles: the tile's positions
       if constexpr (!KEYS) packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
-      int u1 = 0, u2 = 0, b = begin;
-      // behind the last block, one more slot per score buffer says so
-      int last = 0;
-      for (int n = 0; last < ST; ++n) {
-        const int s1 = n % N1, s2 = n % N2, nt = n % NT;
-        if (Role::ALIAS && n == N1 - Role::kAliasSlots)  // X1 has left the slot
-          if (!mbar_wait(xt_full, 0, a.wd, kWdTmaEmpty)) break;
-        if (!mbar_wait(&y1_empty[s1], ((uint32_t)(n / N1) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
-        BwdBlockInfo in = {u1, 0, 0, 0};
-        if (b < 0 || u1 >= count) {
-          info[nt] = in;
-          mbar_arrive(&y1_full[s1]);
-          ++last;
-          continue;
-        }
-        in.row0 = b * BN;
-        in.valid = 1;
-        // Does any pair of the tile and the block need its own mask test?  (Rows
-        // past the slab have nlse = -inf; keys past S matter as Y only: their dS
-        // would meet zero-filled rows, but P of a zero score may overflow.)
-        if constexpr (KEYS) {
-          in.query0 = walk.query(in.row0);
-          const bool wraps = in.query0 + BN > a.L;
-          const int qmin = (wraps ? 0 : in.query0) + a.off, qmax = (wraps ? a.L : in.query0 + BN) - 1 + a.off;
-          in.masked = a.causal && (min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window));
-        } else {
-          in.masked = in.row0 + BN > a.S || (a.causal && in.row0 + BN - 1 > pos_min) ||
-                      (a.window > 0 && pos_max - in.row0 >= a.window);
-        }
-        info[nt] = in;
-        mbar_arrive_expect_tx(&y1_full[s1], Role::kY1Bytes + (KEYS ? 2 * BN * 4 : 0));
-        uint8_t *d1 = sY1 + s1 * Role::kY1Bytes;
+      // Y1 and Y2 are loaded as their slots come free, whichever is first: in one
+      // fixed order a full Y2 ring would hold back the Y1 that the next scores
+      // wait for.  u1 / u2: blocks loaded; behind the last block, one more Y1 slot
+      // per score buffer says that there is none.
+      int u1 = 0, u2 = 0, last = 0, b = begin < 0 || count <= 0 ? -1 : begin, idle = 0;
+      bool alias_free = !Role::ALIAS;
+      uint64_t since = 0;
+      while (last < ST || u2 < u1) {
+        bool moved = false;
+        const int n = u1 + last, s1 = n % N1, nt = n % NT;
+        if (!alias_free && n >= N1 - Role::kAliasSlots) alias_free = mbar_test(xt_full, 0);  // X1 has left the slot
+        if (last < ST && n - u2 < NT && (alias_free || n < N1 - Role::kAliasSlots) &&
+            mbar_test(&y1_empty[s1], ((uint32_t)(n / N1) & 1u) ^ 1u)) {
+          moved = true;
+          BwdBlockInfo in = {u1, parts, 0, 0};
+          if (b < 0) {
+            info[nt] = in;
+            mbar_arrive(&y1_full[s1]);
+            ++last;
+          } else {
+            in.row0 = b * BN;
+            in.valid = 1;
+            // Does any pair of the tile and the block need its own mask test?  (Rows
+            // past the slab have nlse = -inf; keys past S matter as Y only: their dS
+            // would meet zero-filled rows, but P of a zero score may overflow.)
+            if constexpr (KEYS) {
+              in.query0 = walk.query(in.row0);
+              const bool wraps = in.query0 + BN > a.L;
+              const int qmin = (wraps ? 0 : in.query0) + a.off, qmax = (wraps ? a.L : in.query0 + BN) - 1 + a.off;
+              in.masked = a.causal && (min(x0 + kBwdTcRows, a.S) - 1 > qmin || (a.window > 0 && qmax - x0 >= a.window));
+            } else {
+              in.masked = in.row0 + BN > a.S || (a.causal && in.row0 + BN - 1 > pos_min) ||
+                          (a.window > 0 && pos_max - in.row0 >= a.window);
+            }
+            info[nt] = in;
+            mbar_arrive_expect_tx(&y1_full[s1], Role::kY1Bytes + (KEYS ? 2 * BN * 4 : 0));
+            uint8_t *d1 = sY1 + s1 * Role::kY1Bytes;
 #pragma unroll
-        for (int bx = 0; bx < Role::kBoxes1; ++bx)
-          tma_load_3d(d1 + bx * (BN * 128), tm_y1, &y1_full[s1], bx * 64, in.row0, bh);
-        if constexpr (KEYS) {  // row0 + BN <= rpad
-          bulk_load(terms + nt * 2 * BN, nlse + in.row0, BN * 4, &y1_full[s1]);
-          bulk_load(terms + nt * 2 * BN + BN, ndelta + in.row0, BN * 4, &y1_full[s1]);
+            for (int bx = 0; bx < Role::kBoxes1; ++bx)
+              tma_load_3d(d1 + bx * (BN * 128), tm_y1, &y1_full[s1], bx * 64, in.row0, bh);
+            if constexpr (KEYS) {  // row0 + BN <= rpad
+              bulk_load(terms + nt * 2 * BN, nlse + in.row0, BN * 4, &y1_full[s1]);
+              bulk_load(terms + nt * 2 * BN + BN, ndelta + in.row0, BN * 4, &y1_full[s1]);
+            }
+            ++u1;
+            b = u1 < count ? walk.at_or_after(b + 1) : -1;
+          }
         }
-        ++u1;
-        b = walk.at_or_after(b + 1);
-        if (!mbar_wait(&y2_empty[s2], ((uint32_t)(n / N2) & 1u) ^ 1u, a.wd, kWdTmaEmpty)) break;
-        mbar_arrive_expect_tx(&y2_full[s2], Role::kY2Bytes);
-        uint8_t *d2 = sY2 + s2 * Role::kY2Bytes;
+        const int s2 = u2 % N2;
+        if (u2 < u1 && mbar_test(&y2_empty[s2], ((uint32_t)(u2 / N2) & 1u) ^ 1u)) {
+          moved = true;
+          const int row0 = info[u2 % NT].row0;
+          mbar_arrive_expect_tx(&y2_full[s2], Role::kY2Bytes);
+          uint8_t *d2 = sY2 + s2 * Role::kY2Bytes;
 #pragma unroll
-        for (int bx = 0; bx < Role::kBoxes2; ++bx)
-          tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], bx * 64, in.row0, bh);
-        ++u2;
+          for (int bx = 0; bx < Role::kBoxes2; ++bx)
+            tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], bx * 64, row0, bh);
+          ++u2;
+        }
+        if (moved) {
+          idle = 0;
+        } else if ((++idle & 31) == 0) {  // bounded, as every wait
+          const uint64_t now = globaltimer_ns();
+          if (idle == 32) since = now;
+          if (wd_tripped(a.wd)) break;
+          if (now - since > a.wd.limit_ns) {
+            wd_record(a.wd, kWdTmaEmpty);
+            break;
+          }
+        }
       }
       // drain copies still landing (only ever waits after an abort)
       mbar_wait_drain(x_full, 0, a.wd);
@@ -537,7 +575,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         arrive(xt_full);
       }
     }
-    bool any = false;  // the tile has a block
+    int blocks = 0, parts = 1;  // of this CTA; of the tile
     for (uint32_t n = ST == 2 ? group : 0; ok; n += ST) {
       constexpr int kStage = Role::kStageCols;
       const uint32_t st = n % ST, ph = (n / ST) & 1u, slot = n % N1, nt = n % NT;
@@ -548,7 +586,8 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       if (!(ok = wait(&y1_full[slot], (n / N1) & 1u))) break;
       const BwdBlockInfo in = info[nt];
       if (!in.valid) {
-        any = in.row0 > 0;
+        blocks = in.row0;
+        parts = in.query0;
         break;
       }
       float nl[KEYS ? kH : 1];
@@ -644,7 +683,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     }
 
     // ------------------------------ epilogue ------------------------------
-    const bool have = ok && any;
+    const bool have = ok && blocks > 0;
     // (without a block, X may still be landing where the zeros are staged)
     ok = wait(have ? o_final : x_full, 0) && ok;
     const bool have_o = have && ok;
@@ -665,7 +704,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
 #pragma unroll
           for (int e = 0; e < 8; ++e) w8[e] = pack2<kBF16>(o[2 * e] * factor, o[2 * e + 1] * factor);
           stage_16bit_x16(stage, r, c16, w8);
-        } else if (r < nvalid) {  // fp32 sums, [split][slab][row][d]
+        } else if (r < nvalid && split < parts) {  // fp32 sums, [split][slab][row][d]
           float4 *dst = reinterpret_cast<float4 *>(
               out_part + ((((long long)split * a.B * a.Hkv + bh) * xrows + x0 + r) * d + c16 * 16));
 #pragma unroll
@@ -674,12 +713,12 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         }
       }
     };
-    const bool split_out = span.splits > 1;
+    const bool split_out = parts > 1;
     if constexpr (OUT1)
       finish(Role::kOut1Col, Role::D1, bwd_ds_factor<kBF16>(p, gain), smem + Role::kStage1Off, split_out ? span.part1 : nullptr);
     if constexpr (OUT2)
       finish(Role::kOut2Col, Role::D2, bwd_dv_factor<kBF16>(), smem + Role::kStage2Off, split_out ? span.part2 : nullptr);
-    if (!split_out) {
+    if (!split_out && split == 0) {
       fence_proxy_async_smem();
       asm volatile("bar.sync 1, %0;" ::"n"(kBwdTcSoftmaxWarps * 32) : "memory");
       // rows past the slab and columns past the head dim are clipped
@@ -758,7 +797,8 @@ struct BwdTcRoles<256, 256> {
 template <bool kBF16, int DQK, int DV>
 __global__ void __launch_bounds__(kBwdTcThreads, 1)
     bwd_tc_kernel(const __grid_constant__ BwdTcMaps tm, const __grid_constant__ BwdParams p,
-                  const __grid_constant__ BwdTcSpan keys, const __grid_constant__ BwdTcSpan rows) {
+                  const __grid_constant__ BwdTcSpan keys, const __grid_constant__ BwdTcSpan rows,
+                  const int rows_first) {
   using Roles = BwdTcRoles<DQK, DV>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // The 128-byte swizzle atoms need 1024-byte aligned tiles; see tc.cuh.
@@ -768,38 +808,44 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
   }
   const int slabs = p.a.B * p.a.Hkv;
   const int key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
+  // the kind with the longest block lists first
   int id = blockIdx.x;
+  if (rows_first) id = id < row_ctas ? (int)gridDim.x - row_ctas + id : id - row_ctas;
   if (id < key_ctas) {
     bwd_tc_tile<kBF16, typename Roles::Key>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
     return;
   }
   id -= key_ctas;
-  if (id < row_ctas) {
-    bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.qx, &tm.dox, &tm.ky, &tm.vy, &tm.dq, &tm.dq, rows, id, smem_raw);
-    return;
-  }
   if constexpr (!std::is_void_v<typename Roles::KeyV>) {
-    id -= row_ctas;
-    bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
+    if (id < key_ctas) {
+      bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
+      return;
+    }
+    id -= key_ctas;
   }
+  bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.qx, &tm.dox, &tm.ky, &tm.vy, &tm.dq, &tm.dq, rows, id, smem_raw);
 }
 
-// Sum of the splits' fp32 tiles, times the factor, rounded once: X rows of all
+// Sum of a tile's parts, where it has several, times the factor, rounded once: X rows of all
 // slabs, d columns (a multiple of 8; the tiles' rows are dpad wide).
 template <bool kBF16>
 __global__ void __launch_bounds__(256)
     bwd_join_kernel(const BwdParams p, const float *__restrict__ part, uint16_t *__restrict__ out,
-                    long long rows, int rows_per_slab, int d, int dpad, int splits, int is_dv) {
+                    const int *__restrict__ parts, int tiles, long long rows, int rows_per_slab, int d,
+                    int dpad, int is_dv) {
   const int per_row = d / 4;
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   if (id >= rows * per_row) return;
   const long long row = id / per_row;
   const int c = (int)(id - row * per_row) * 4;
+  const int slab = (int)(row / rows_per_slab);
+  const int n = parts[slab * tiles + (int)(row - (long long)slab * rows_per_slab) / kBwdTcRows];
+  if (n <= 1) return;  // written by its one part
   const float4 *src = reinterpret_cast<const float4 *>(part + row * dpad + c);
   const long long stride = rows * dpad / 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < splits; ++i) {
+  for (int i = 0; i < n; ++i) {
     const float4 x = __ldcs(src + i * stride);
     s.x += x.x;
     s.y += x.y;
@@ -807,7 +853,7 @@ __global__ void __launch_bounds__(256)
     s.w += x.w;
   }
   const float f = is_dv ? bwd_dv_factor<kBF16>()
-                        : bwd_ds_factor<kBF16>(p, bwd_gain<kBF16>(p, (int)(row / rows_per_slab)));
+                        : bwd_ds_factor<kBF16>(p, bwd_gain<kBF16>(p, slab));
   uint2 w;
   w.x = pack2<kBF16>(s.x * f, s.y * f);
   w.y = pack2<kBF16>(s.z * f, s.w * f);

@@ -12,9 +12,12 @@ struct BwdPlan {
   int rows;   // packed query rows per (batch, KV head)
   int rpad;   // ... rounded up so that every tile and block stays inside
   int pair;   // tcgen05 path: index into kDimPairs
-  int key_splits, row_splits;  // parts of a key / query tile's block list
+  int key_splits, row_splits;  // parts of the longest block list of a key / query tile
+  int key_per, row_per;        // blocks of a part
+  int rows_first;              // the query tiles have the longer lists: first in the grid
   size_t row_bytes, norm_bytes;
-  size_t key_part1_bytes, key_part2_bytes, row_part_bytes;  // fp32 sums of the parts
+  size_t count_bytes;  // parts of each tile
+  size_t key_part1_bytes, key_part2_bytes, row_part_bytes;  // their fp32 sums
   size_t ws_bytes;
 };
 
@@ -26,6 +29,7 @@ struct BwdLaunch {
   const float *lse, *dlse;
   float *nlse, *ndelta;
   unsigned int *norms;
+  int *key_parts, *row_parts;
   float *key_part1, *key_part2, *row_part;
   int sms;
   unsigned int *wd_word;

@@ -7,15 +7,15 @@ namespace sdpa {
 namespace {
 
 template <bool kBF16>
-cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const float *part, void *out, int rows_per_slab,
-                 int d, int dpad, int splits, int is_dv) {
+cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const BwdTcSpan &span, const float *part, void *out,
+                 int rows_per_slab, int d, int dpad, int is_dv) {
   const long long rows = (long long)ln.pb.B * ln.pb.Hkv * rows_per_slab;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows * (d / 4) + 255) / 256));
   cfg.blockDim = dim3(256);
   cfg.stream = ln.stream;
-  return cudaLaunchKernelEx(&cfg, bwd_join_kernel<kBF16>, p, part, (uint16_t *)out, rows, rows_per_slab, d,
-                            dpad, splits, is_dv);
+  return cudaLaunchKernelEx(&cfg, bwd_join_kernel<kBF16>, p, part, (uint16_t *)out, (const int *)span.parts,
+                            span.tiles, rows, rows_per_slab, d, dpad, is_dv);
 }
 
 template <bool kBF16, int DQK, int DV>
@@ -33,9 +33,8 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   BwdParams p;
   fill_bwd_params(ln, &p);
   const long long slabs = (long long)pb.B * pb.Hkv;
-  BwdTcSpan keys = {(pb.S + 127) / 128, pl.key_splits, pl.key_splits > 1 ? ln.key_part1 : nullptr,
-                    pl.key_splits > 1 ? ln.key_part2 : nullptr};
-  BwdTcSpan rows = {(pl.rows + 127) / 128, pl.row_splits, pl.row_splits > 1 ? ln.row_part : nullptr, nullptr};
+  BwdTcSpan keys = {(pb.S + 127) / 128, pl.key_splits, pl.key_per, ln.key_parts, ln.key_part1, ln.key_part2};
+  BwdTcSpan rows = {(pl.rows + 127) / 128, pl.row_splits, pl.row_per, ln.row_parts, ln.row_part, nullptr};
   const long long key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
   const long long ctas = key_ctas * (std::is_void_v<typename Roles::KeyV> ? 1 : 2) + row_ctas;
   const long long join_ctas = slabs * (pb.S > pl.rows ? (long long)pb.S : pl.rows) * 64 / 256;
@@ -70,13 +69,13 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm, p, keys, rows);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm, p, keys, rows, pl.rows_first);
   if (e == cudaSuccess && pl.key_splits > 1)
-    e = join<kBF16>(ln, p, keys.part1, ln.dk, S, Dqk, DQK, pl.key_splits, 0);
+    e = join<kBF16>(ln, p, keys, keys.part1, ln.dk, S, Dqk, DQK, 0);
   if (e == cudaSuccess && pl.key_splits > 1)
-    e = join<kBF16>(ln, p, keys.part2, ln.dv, S, Dv, DV, pl.key_splits, 1);
+    e = join<kBF16>(ln, p, keys, keys.part2, ln.dv, S, Dv, DV, 1);
   if (e == cudaSuccess && pl.row_splits > 1)
-    e = join<kBF16>(ln, p, rows.part1, ln.dq, R, Dqk, DQK, pl.row_splits, 0);
+    e = join<kBF16>(ln, p, rows, rows.part1, ln.dq, R, Dqk, DQK, 0);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     *err = std::string("bwd_tc_kernel launch failed: ") + cudaGetErrorString(e);

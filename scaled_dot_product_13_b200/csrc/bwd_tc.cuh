@@ -294,7 +294,13 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   const int x0 = tile * kBwdTcRows;
   const int xrows = KEYS ? a.S : a.R;
 
-  if (threadIdx.x == 0) {
+  // The producer sets up the barriers and requests X while the MMA warp takes its
+  // tensor memory.  (Launched as a programmatic dependent of the row-term kernel:
+  // nothing before the wait touches global memory.)
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(tm_x1);
+    tma_prefetch_desc(tm_y1);
+    tma_prefetch_desc(tm_y2);
     for (int s = 0; s < N1; ++s) {
       mbar_init(&y1_full[s], 1);
       mbar_init(&y1_empty[s], 1);
@@ -314,6 +320,16 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     mbar_init(o_final, 1);
     mbar_init(fin_bar, 1);
     fence_barrier_init();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    mbar_arrive_expect_tx(x_full, Role::kX1Bytes + Role::kX2Bytes);
+#pragma unroll
+    for (int bx = 0; bx < Role::kBoxes1; ++bx)
+      tma_load_3d(sX1 + bx * (128 * 128), tm_x1, x_full, bx * 64, x0, bh);
+    if constexpr (OUT1) {
+#pragma unroll
+      for (int bx = 0; bx < Role::kBoxes2; ++bx)
+        tma_load_3d(sX2 + bx * (128 * 128), tm_x2, x_full, bx * 64, x0, bh);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
@@ -323,25 +339,11 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  // launched as a programmatic dependent of the row-term kernel: nothing below
-  // touches global memory before that grid has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kProducerWarp) {
     // ============================ TMA producer ============================
     if (lane == 0) {
-      tma_prefetch_desc(tm_x1);
-      tma_prefetch_desc(tm_y1);
-      tma_prefetch_desc(tm_y2);
-      mbar_arrive_expect_tx(x_full, Role::kX1Bytes + Role::kX2Bytes);
-#pragma unroll
-      for (int bx = 0; bx < Role::kBoxes1; ++bx)
-        tma_load_3d(sX1 + bx * (128 * 128), tm_x1, x_full, bx * 64, x0, bh);
-      if constexpr (OUT1) {
-#pragma unroll
-        for (int bx = 0; bx < Role::kBoxes2; ++bx)
-          tma_load_3d(sX2 + bx * (128 * 128), tm_x2, x_full, bx * 64, x0, bh);
-      }
       const float *nlse = p.nlse + (long long)bh * p.rpad;
       const float *ndelta = p.ndelta + (long long)bh * p.rpad;
       // the block list of this CTA: `count` visited blocks from `begin`
@@ -730,7 +732,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           for (int bx = 0; bx < Role::kBoxes2 && bx * 64 < a.Dv; ++bx)
             tma_store_3d(tm_o2, smem + Role::kStage2Off + bx * (128 * 128), bx * 64, x0, bh);
         bulk_commit_group();
-        bulk_wait_group0();
+        bulk_wait_group_read0();  // the staging may go; the grid's end completes the writes
       }
     }
   }

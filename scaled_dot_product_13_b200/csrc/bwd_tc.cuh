@@ -483,57 +483,93 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     };
     bool ok = wait(x_full, 0, kWdTmaFull);
     if (XT) ok = ok && wait(xt_full, 0, kWdSoftmax);
-    // one loop, so that each product's code is there once: step m issues the
-    // second products of block m and the first ones of block m + ST
-    int issued = 0, n = 0;
-    bool more = true;
-    for (int m = -ST; ok && (m < 0 || m < issued); ++m) {
-      const uint32_t um = (uint32_t)m, un = (uint32_t)(m + ST);
-      const bool have = m >= 0;
-      const int s1 = um % N1, s2 = um % N2, st = un % ST, t1 = un % N1, t2 = un % N2;
-      const uint32_t ph = (um / ST) & 1u;
-      // Y1 of block m + ST, which is as a rule there long before P_m
-      if (have && more)
-        ok = mbar_wait_warp2(&p_full[st], ph, kWdSoftmax, &y1_full[t1], (un / N1) & 1u, kWdTmaFull, a.wd);
-      else if (have)
-        ok = wait(&p_full[st], ph, kWdSoftmax);
-      else if (more)
-        ok = wait(&y1_full[t1], (un / N1) & 1u, kWdTmaFull);
-      if (!ok) break;
-      if (OUT2 && have) {
-        if constexpr (!OUT1)
-          if (!(ok = wait(&y2_full[s2], (um / N2) & 1u, kWdTmaFull))) break;
-        second(st * Role::kStageCols, y2 + s2 * Role::kY2Bytes, Role::kOut2Col, kIdesc2, m == 0);
-        tc_commit_warp(leader, &y2_empty[s2]);
+    // First products of block i (into score buffer st): false behind the last.
+    // Slots and parities run along as counters: what is computed between two
+    // products, and the latency of a wait, drains the tensor pipe, which holds
+    // only about four issued MMAs.
+    struct Ring {
+      uint32_t slot, parity;
+      __device__ __forceinline__ void step(uint32_t n) {
+        if (++slot == n) {
+          slot = 0;
+          parity ^= 1u;
+        }
       }
-      if (more) more = __any_sync(0xffffffffu, info[un % NT].valid);
-      if (more) {
-        first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
-              y1 + t1 * Role::kY1Bytes, st * Role::kStageCols);
-        tc_commit_warp(leader, &s_full[st]);
-        if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[t1]);
-        ++issued;
-      }
+    };
+    Ring r1 = {0, 0}, r2 = {0, 0}, rt = {0, 0};  // Y1, Y2 and note of the next block to start
+    auto start_s = [&](uint32_t st) {
+      first(std::bool_constant<Role::XT1>(), std::integral_constant<int, Role::D1>(), Role::XT1 ? Role::kX1Col : x1,
+            y1 + r1.slot * Role::kY1Bytes, st * Role::kStageCols);
+      tc_commit_warp(leader, &s_full[st]);
+      if constexpr (!OUT1) tc_commit_warp(leader, &y1_empty[r1.slot]);
+    };
+    auto start_dp = [&](uint32_t st, uint32_t slot) {
+      first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
+            y2 + slot * Role::kY2Bytes, st * Role::kStageCols + BN);
+      tc_commit_warp(leader, &dp_full[st]);
+      if constexpr (!OUT2) tc_commit_warp(leader, &y2_empty[slot]);
+    };
+    int started = 0;
+    bool more = ok;
+    for (uint32_t st = 0; st < ST && more; ++st) {
+      if (!(ok = wait(&y1_full[r1.slot], r1.parity, kWdTmaFull))) break;
+      if (!(more = __any_sync(0xffffffffu, info[rt.slot].valid))) break;
+      start_s(st);
       if constexpr (OUT1) {
-        if (have && more)
-          ok = mbar_wait_warp2(&ds_full[st], ph, kWdSoftmax, &y2_full[t2], (un / N2) & 1u, kWdTmaFull, a.wd);
-        else if (have)
-          ok = wait(&ds_full[st], ph, kWdSoftmax);
-        else if (more)
-          ok = wait(&y2_full[t2], (un / N2) & 1u, kWdTmaFull);
-        if (!ok) break;
-        if (have) {
-          second(st * Role::kStageCols + BN, y1 + s1 * Role::kY1Bytes, Role::kOut1Col, kIdesc1, m == 0);
-          tc_commit_warp(leader, &y1_empty[s1]);
-        }
-        if (more) {
-          first(std::bool_constant<Role::XT2>(), std::integral_constant<int, Role::D2>(), Role::XT2 ? Role::kX2Col : x2,
-                y2 + t2 * Role::kY2Bytes, st * Role::kStageCols + BN);
-          tc_commit_warp(leader, &dp_full[st]);
-          if constexpr (!OUT2) tc_commit_warp(leader, &y2_empty[t2]);
-        }
+        if (!(ok = wait(&y2_full[r2.slot], r2.parity, kWdTmaFull))) break;
+        start_dp(st, r2.slot);
       }
-      if (have) ++n;
+      ++started;
+      r1.step(N1);
+      r2.step(N2);
+      rt.step(NT);
+    }
+    // step n: second products of block n, first ones of block n + ST
+    Ring c1 = {0, 0}, c2 = {0, 0}, cs = {0, 0};  // Y1, Y2 and score buffer of block n
+    int n = 0;
+    bool ready = false;  // P_n (and Y1 of block n + ST) seen complete under the last product
+    while (ok && n < started) {
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = more ? mbar_wait_warp2(&p_full[cs.slot], cs.parity, kWdSoftmax, &y1_full[r1.slot], r1.parity, kWdTmaFull, a.wd)
+                  : wait(&p_full[cs.slot], cs.parity, kWdSoftmax);
+        if (!ok) break;
+      }
+      if constexpr (OUT2) {
+        if constexpr (!OUT1)
+          if (!(ok = wait(&y2_full[c2.slot], c2.parity, kWdTmaFull))) break;
+        second(cs.slot * Role::kStageCols, y2 + c2.slot * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
+        tc_commit_warp(leader, &y2_empty[c2.slot]);
+      }
+      bool ds_ready = false;
+      if (more) {
+        if constexpr (OUT1)
+          ds_ready = mbar_test(&ds_full[cs.slot], cs.parity) && mbar_test(&y2_full[r2.slot], r2.parity);
+        more = __any_sync(0xffffffffu, info[rt.slot].valid);
+      }
+      if (more) {
+        start_s(cs.slot);
+        ++started;
+        r1.step(N1);
+        rt.step(NT);
+      }
+      const uint32_t st = cs.slot, y2_next = r2.slot;
+      if constexpr (OUT1) {
+        if (!__all_sync(0xffffffffu, ds_ready)) {
+          ok = more ? mbar_wait_warp2(&ds_full[st], cs.parity, kWdSoftmax, &y2_full[y2_next], r2.parity, kWdTmaFull, a.wd)
+                    : wait(&ds_full[st], cs.parity, kWdSoftmax);
+          if (!ok) break;
+        }
+        second(st * Role::kStageCols + BN, y1 + c1.slot * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
+        tc_commit_warp(leader, &y1_empty[c1.slot]);
+      }
+      ++n;
+      c1.step(N1);
+      c2.step(N2);
+      cs.step(ST);
+      if (more) r2.step(N2);
+      ready = more && mbar_test(&p_full[cs.slot], cs.parity) && mbar_test(&y1_full[r1.slot], r1.parity);
+      if constexpr (OUT1)
+        if (more) start_dp(st, y2_next);
     }
     if (ok && n > 0) tc_commit_warp(leader, o_final);
     // all MMAs of this CTA complete before TMEM is released

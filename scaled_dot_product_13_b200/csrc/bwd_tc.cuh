@@ -592,7 +592,10 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       pos = (x0 + r) % a.L + a.off;
     }
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-      const bool w = mbar_wait_warp(bar, parity, a.wd, kWdMma);
+      // (the waiting loop in line here: with the MMA warp's it took head dims 256
+      // 5 % longer)
+      bool w = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity));
+      if (!w) w = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wd, kWdMma));
       tc_fence_after();
       return w;
     };

@@ -128,22 +128,48 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
   }
 }
 
-// The same wait by a whole converged warp; the result is uniform.  The common
-// case (the phase has completed) is one try and one vote without a taken branch.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, const Watchdog &wd,
-                                               uint32_t code) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, code));
+// Out of line: the waiting loop is a few hundred bytes of code that a tight
+// role (the MMA issuer) should not have between its instructions.
+static __device__ __noinline__ bool mbar_wait_far(uint32_t bar, uint32_t parity, unsigned int *word,
+                                                  uint64_t limit_ns, uint32_t code) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    const Watchdog wd = {word, limit_ns};
+    if (wd_tripped(wd)) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      wd_record(wd, code);
+      return false;
+    }
+  }
 }
 
-// Both of two barriers: the two tries overlap (one satisfied wait costs 72
-// cycles, nearly all of it the try's latency).
+// The same wait by a whole converged warp; the result is uniform.  The usual waits
+// end in the first tries (72 cycles where the phase had completed); the loop that
+// watches the clock is out of line.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, const Watchdog &wd,
+                                               uint32_t code) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_far(a, parity, wd.word, wd.limit_ns, code));
+}
+
+// Both of two barriers: the two tries overlap.
 __device__ __forceinline__ bool mbar_wait_warp2(uint64_t *bar, uint32_t parity, uint32_t code,
                                                 uint64_t *bar2, uint32_t parity2, uint32_t code2,
                                                 const Watchdog &wd) {
-  const bool a = mbar_try_wait(smem_u32(bar), parity), b = mbar_try_wait(smem_u32(bar2), parity2);
-  if (__all_sync(0xffffffffu, a && b)) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, code) && mbar_wait(bar2, parity2, wd, code2));
+  const uint32_t a = smem_u32(bar), b = smem_u32(bar2);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i) {
+    const bool x = mbar_try_wait(a, parity), y = mbar_try_wait(b, parity2);
+    if (__all_sync(0xffffffffu, x && y)) return true;
+  }
+  return __all_sync(0xffffffffu, mbar_wait_far(a, parity, wd.word, wd.limit_ns, code) &&
+                                     mbar_wait_far(b, parity2, wd.word, wd.limit_ns, code2));
 }
 
 // Teardown wait: only the time limit ends it (used to drain in-flight copies

@@ -117,9 +117,9 @@ struct BwdTcRole {
 };
 
 struct BwdTcMaps {
-  CUtensorMap kx, vx, qy, doy;  // key tiles: X boxes of 128 rows, Y boxes of the kind's BN
-  CUtensorMap qx, dox, ky, vy;  // query tiles
-  CUtensorMap dq, dk, dv;       // 128-row boxes
+  CUtensorMap q, k, v, dout;  // boxes of 64 rows: X tiles (two high), blocks of 64 rows
+  CUtensorMap qb, doutb;      // boxes of a key tile's blocks where those are not of 64 rows
+  CUtensorMap dq, dk, dv;     // boxes of 128 rows
 };
 
 // Tiles of one kind within the grid.
@@ -323,12 +323,12 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     asm volatile("griddepcontrol.wait;" ::: "memory");
     mbar_arrive_expect_tx(x_full, Role::kX1Bytes + Role::kX2Bytes);
 #pragma unroll
-    for (int bx = 0; bx < Role::kBoxes1; ++bx)
-      tma_load_3d(sX1 + bx * (128 * 128), tm_x1, x_full, bx * 64, x0, bh);
+    for (int bx = 0; bx < 2 * Role::kBoxes1; ++bx)
+      tma_load_3d(sX1 + bx * (64 * 128), tm_x1, x_full, (bx >> 1) * 64, x0 + (bx & 1) * 64, bh);
     if constexpr (OUT1) {
 #pragma unroll
-      for (int bx = 0; bx < Role::kBoxes2; ++bx)
-        tma_load_3d(sX2 + bx * (128 * 128), tm_x2, x_full, bx * 64, x0, bh);
+      for (int bx = 0; bx < 2 * Role::kBoxes2; ++bx)
+        tma_load_3d(sX2 + bx * (64 * 128), tm_x2, x_full, (bx >> 1) * 64, x0 + (bx & 1) * 64, bh);
     }
   }
   if (warp == kMmaWarp) {
@@ -849,22 +849,23 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
   }
   const int slabs = p.a.B * p.a.Hkv;
   const int key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
+  const CUtensorMap *qb = Roles::Key::BN == 64 ? &tm.q : &tm.qb, *doutb = Roles::Key::BN == 64 ? &tm.dout : &tm.doutb;
   // the kind with the longest block lists first
   int id = blockIdx.x;
   if (rows_first) id = id < row_ctas ? (int)gridDim.x - row_ctas + id : id - row_ctas;
   if (id < key_ctas) {
-    bwd_tc_tile<kBF16, typename Roles::Key>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
+    bwd_tc_tile<kBF16, typename Roles::Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
     return;
   }
   id -= key_ctas;
   if constexpr (!std::is_void_v<typename Roles::KeyV>) {
     if (id < key_ctas) {
-      bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.kx, &tm.vx, &tm.qy, &tm.doy, &tm.dk, &tm.dv, keys, id, smem_raw);
+      bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
       return;
     }
     id -= key_ctas;
   }
-  bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.qx, &tm.dox, &tm.ky, &tm.vy, &tm.dq, &tm.dq, rows, id, smem_raw);
+  bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
 }
 
 // Sum of a tile's parts, where it has several, times the factor, rounded once: X rows of all

@@ -48,16 +48,19 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
     const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
     return encode_tma(m, pb.dtype, 3, base, dims, strides, box, err);
   };
-  constexpr int BK = Roles::Key::BN, BQ = Roles::Query::BN;
+  constexpr int BK = Roles::Key::BN;
   const int R = pl.rows, S = pb.S, Dqk = pb.Dqk, Dv = pb.Dv;
   BwdTcMaps tm;
-  if (!map(&tm.kx, ln.k, Dqk, S, 128) || !map(&tm.vx, ln.v, Dv, S, 128) ||
-      !map(&tm.qy, ln.q, Dqk, R, BK) || !map(&tm.doy, ln.dout, Dv, R, BK) ||
-      !map(&tm.qx, ln.q, Dqk, R, 128) || !map(&tm.dox, ln.dout, Dv, R, 128) ||
-      !map(&tm.ky, ln.k, Dqk, S, BQ) || !map(&tm.vy, ln.v, Dv, S, BQ) ||
-      !map(&tm.dq, ln.dq, Dqk, R, 128) || !map(&tm.dk, ln.dk, Dqk, S, 128) ||
-      !map(&tm.dv, ln.dv, Dv, S, 128))
+  if (!map(&tm.q, ln.q, Dqk, R, 64) || !map(&tm.k, ln.k, Dqk, S, 64) || !map(&tm.v, ln.v, Dv, S, 64) ||
+      !map(&tm.dout, ln.dout, Dv, R, 64) || !map(&tm.dq, ln.dq, Dqk, R, 128) ||
+      !map(&tm.dk, ln.dk, Dqk, S, 128) || !map(&tm.dv, ln.dv, Dv, S, 128))
     return SDPA_ERR_CUDA;
+  if (BK == 64) {
+    tm.qb = tm.q;
+    tm.doutb = tm.dout;
+  } else if (!map(&tm.qb, ln.q, Dqk, R, BK) || !map(&tm.doutb, ln.dout, Dv, R, BK)) {
+    return SDPA_ERR_CUDA;
+  }
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);

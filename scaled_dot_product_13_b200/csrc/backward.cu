@@ -35,16 +35,16 @@ sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *o
     return refuse(SDPA_ERR_INVALID_ARG, "unknown backward path");
   pl.pair = 0;
   while (pl.pair < kNumDimPairs && (kDimPairs[pl.pair].dqk < pb.Dqk || kDimPairs[pl.pair].dv < pb.Dv)) ++pl.pair;
-  const bool tc_fits = pl.pair < kWidePair && rows < (1 << 30) && pb.S < (1 << 30);
+  const bool tc_fits = rows < (1 << 30) && pb.S < (1 << 30);
   if (force_path == SDPA_BWD_PATH_TC && !tc_fits)
-    return refuse(SDPA_ERR_UNSUPPORTED, "the tcgen05 backward path is built for head dims up to 256 and up to 2^30 rows and keys");
+    return refuse(SDPA_ERR_UNSUPPORTED, "the tcgen05 backward path is built for up to 2^30 rows and keys");
   pl.path = force_path != SDPA_BWD_PATH_AUTO ? force_path : tc_fits ? SDPA_BWD_PATH_TC : SDPA_BWD_PATH_TILE;
   pl.rpad = (pl.rows + 127) / 128 * 128;
   pl.key_splits = pl.row_splits = 1;
   const size_t slabs = (size_t)pb.B * pb.Hkv;
   if (pl.path == SDPA_BWD_PATH_TC) {
     const DimPair dp = kDimPairs[pl.pair];
-    const int bk = bwd_tc_key_block(dp.dqk, dp.dv), bq = kBwdTcQueryBlock;
+    const int bk = bwd_tc_key_block(dp.dqk, dp.dv), bq = bwd_tc_query_block(dp.dqk);
     if (128 % bk != 0) pl.rpad += 128;  // 48-row blocks end up to 47 rows behind the slab
     // Split a tile's block list where one tile would outlast the whole grid's
     // work spread over the SMs (few tiles with long lists: few query rows over

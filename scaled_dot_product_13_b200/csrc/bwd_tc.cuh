@@ -59,19 +59,29 @@ constexpr int kBwdTcSoftmaxWarps = 8;
 constexpr int kBwdTcThreads = (kBwdTcSoftmaxWarps + 2) * 32;
 
 // One kind of tile.  ST: score buffers; N1 / N2: ring slots of Y1 and Y2;
-// XT1 / XT2: X1 / X2 are read from TMEM; ALIAS: X1 passes through the last Y1
+// XT1 / XT2: X1 / X2 are read from TMEM; W: gradient columns of a CTA where several
+// share a tile (0: all); ALIAS: X1 passes through the last Y1
 // slots on its way there.
 template <int D1_, int D2_, int BN_, int ST_, int N1_, int N2_, bool KEYS_, bool OUT1_, bool OUT2_, bool XT1_, bool XT2_,
-          bool ALIAS_ = false>
+          bool ALIAS_ = false, int W_ = 0>
 struct BwdTcRole {
   static constexpr int D1 = D1_, D2 = D2_, BN = BN_, ST = ST_, N1 = N1_, N2 = N2_;
   static constexpr bool KEYS = KEYS_, OUT1 = OUT1_, OUT2 = OUT2_, XT1 = XT1_, XT2 = XT2_, ALIAS = ALIAS_;
   static constexpr int kBoxes1 = (D1 + 63) / 64, kBoxes2 = (D2 + 63) / 64;
+  static constexpr int W1 = W_ ? W_ : D1, W2 = W_ ? W_ : D2;  // columns of out1, out2
+  static constexpr bool PARTED = W_ != 0;
+  static constexpr int kBoxRows = BN == 32 ? 32 : 64;  // of the tensor maps of X and Y
   static constexpr uint32_t kX1Bytes = kBoxes1 * 128 * 128;
   static constexpr uint32_t kX2Bytes = OUT1 ? kBoxes2 * 128 * 128 : 0;  // dP only
   static constexpr uint32_t kY1Bytes = kBoxes1 * BN * 128;
-  static constexpr uint32_t kY2Bytes = kBoxes2 * BN * 128;
-  static constexpr int kAliasSlots = ALIAS ? (kX1Bytes + kY1Bytes - 1) / kY1Bytes : 0;
+  // (without dP, only the columns of out2 are needed of Y2)
+  static constexpr int kY2Boxes = OUT1 ? kBoxes2 : (W2 + 63) / 64;
+  static constexpr uint32_t kY2Bytes = kY2Boxes * BN * 128;
+  // X1 goes through the rings in one pass, or (both rings being smaller) in two
+  static constexpr int kXFirst = ALIAS && N1 * kY1Bytes + N2 * kY2Bytes < kX1Bytes
+                                     ? (N1 * kY1Bytes + N2 * kY2Bytes) / (128 * 128) : kBoxes1;
+  static constexpr bool TWICE = kXFirst < kBoxes1;
+  static constexpr int kAliasSlots = !ALIAS ? 0 : TWICE ? N1 : (kX1Bytes + kY1Bytes - 1) / kY1Bytes;
   static constexpr uint32_t kX2Off = ALIAS ? 0 : kX1Bytes;
   static constexpr uint32_t kY1Off = kX2Off + kX2Bytes;
   static constexpr uint32_t kX1Off = ALIAS ? kY1Off + (N1 - kAliasSlots) * kY1Bytes : 0;
@@ -83,12 +93,12 @@ struct BwdTcRole {
   static constexpr uint32_t kTermBytes = KEYS ? NT * 2 * BN * 4 : 0;
   static constexpr uint32_t kInfoOff = kTermOff + kTermBytes;  // [NT] BwdBlockInfo
   static constexpr uint32_t kBarOff = kInfoOff + NT * 16;
-  static constexpr int kNumBars = 2 * N1 + 2 * N2 + 4 * ST + 4;
+  static constexpr int kNumBars = 2 * N1 + 2 * N2 + 4 * ST + 6;
   static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 16;
   static constexpr int kStageCols = OUT1 ? 2 * BN : BN;  // S and dP of one stage
   static constexpr int kOut1Col = ST * kStageCols;
-  static constexpr int kOut2Col = kOut1Col + (OUT1 ? D1 : 0);
-  static constexpr int kX1Col = kOut2Col + (OUT2 ? D2 : 0);
+  static constexpr int kOut2Col = kOut1Col + (OUT1 ? W1 : 0);
+  static constexpr int kX1Col = kOut2Col + (OUT2 ? W2 : 0);
   static constexpr int kX2Col = kX1Col + (XT1 ? D1 / 2 : 0);
   static constexpr int kColsUsed = kX2Col + (XT2 ? D2 / 2 : 0);
   static constexpr int kParts = ST == 1 ? 2 : 1;  // softmax warps sharing a row
@@ -103,16 +113,17 @@ struct BwdTcRole {
   static_assert(kColsUsed <= 512, "TMEM columns");
   // Y1_n is held until out1_n (without out1, until S_n), issued after S_{n+ST}
   static_assert(N1 >= ST + 1 && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
-  static_assert(!ALIAS || (XT1 && OUT1 && !OUT2 && kX2Bytes >= kX1Bytes && N1 > kAliasSlots), "");
-  static_assert(OUT1 || kBoxes2 <= kBoxes1, "out2's staging");
+  static_assert(!ALIAS || (XT1 && OUT1 != OUT2 && N1 >= kAliasSlots && kXFirst >= kBoxes1 - kXFirst), "");
+  static_assert(W1 % 16 == 0 && W2 % 16 == 0 && (!PARTED || W1 % 64 == 0), "");
+  static_assert(OUT1 || kY2Boxes <= kBoxes1, "out2's staging");
   static_assert(!XT2 || OUT1, "");
   static_assert(kH % 16 == 0 && BN % 16 == 0, "");
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct BwdTcMaps {
-  CUtensorMap q, k, v, dout;  // boxes of 64 rows: X tiles (two high), blocks of 64 rows
-  CUtensorMap qb, doutb;      // boxes of a key tile's blocks where those are not of 64 rows
+  CUtensorMap q, k, v, dout;  // boxes of 64 rows (head dims 512: 32): X tiles, blocks
+  CUtensorMap qb, doutb;      // boxes of a key tile's blocks where those have other rows
   CUtensorMap dq, dk, dv;     // boxes of 128 rows
 };
 
@@ -218,14 +229,16 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, float *v) {
 
 // X (boxes of 128 rows x 64 columns, 128-byte swizzled) to TMEM as the A operand of
 // a first product: 16-bit pairs, a row per lane.  Four warps, one row per thread.
-template <int D>
+// Columns [16 C0, 16 C1); x holds the boxes from column 16 C0 on.
+template <int C0, int C1>
 __device__ __forceinline__ void bwd_x_to_tmem(const uint8_t *x, uint32_t taddr, int r) {
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
+  static_assert(C0 % 4 == 0, "whole boxes");
+#pragma unroll 8
+  for (int c = C0; c < C1; ++c) {
     uint32_t v[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int chunk = c * 2 + i;
+      const int chunk = (c - C0) * 2 + i;
       const uint4 t = *reinterpret_cast<const uint4 *>(x + (chunk >> 3) * (128 * 128) + sw128_offset(r, chunk & 7));
       v[4 * i] = t.x;
       v[4 * i + 1] = t.y;
@@ -261,7 +274,9 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   uint64_t *xt_full = x_full + 1;   // X copied to TMEM
   uint64_t *o_final = xt_full + 1;  // every product has completed
   uint64_t *fin_bar = o_final + 1;  // teardown drain of the MMA warp
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin_bar + 1);
+  uint64_t *xh_empty = fin_bar + 1;  // X1 in two passes: the first one copied ...
+  uint64_t *xh_full = xh_empty + 1;  // ... the second one there
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xh_full + 1);
   constexpr int kProducerWarp = kBwdTcSoftmaxWarps, kMmaWarp = kBwdTcSoftmaxWarps + 1;
   constexpr bool XT = Role::XT1 || Role::XT2;
   // (through a shuffle, so that the compiler knows the roles' branches to be
@@ -272,7 +287,12 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   // while its tiles run), then split, then slab.  Query tiles, which run last and
   // read the smaller K and V: slab fastest, so that the grid ends with the tiles
   // of fewest blocks.  The tiles that visit most blocks come first in both ---
-  int tile, split, bh;
+  int tile, split, bh, col_part = 0;
+  if constexpr (Role::PARTED) {  // the parts of a tile next to each other
+    const int parts = ((OUT1 ? a.Dqk : a.Dv) + Role::W1 - 1) / Role::W1;
+    col_part = id % parts;
+    id /= parts;
+  }
   if (KEYS) {
     tile = id % span.tiles;
     id /= span.tiles;
@@ -288,6 +308,12 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   const int x0 = tile * kBwdTcRows;
   const int xrows = KEYS ? a.S : a.R;
 
+  // box `bx` of an X tile (128 rows of 64 columns) into the place of box bx - first
+  auto load_x = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int bx, int first) {
+#pragma unroll
+    for (int row = 0; row < 128; row += Role::kBoxRows)
+      tma_load_3d(dst + (bx - first) * (128 * 128) + row * 128, map, bar, bx * 64, x0 + row, bh);
+  };
   // The producer sets up the barriers and requests X while the MMA warp takes its
   // tensor memory.  (Launched as a programmatic dependent of the row-term kernel:
   // nothing before the wait touches global memory.)
@@ -313,16 +339,16 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     mbar_init(xt_full, 4 * ((Role::XT1 ? 1 : 0) + (Role::XT2 ? 1 : 0)) + (XT ? 0 : 1));
     mbar_init(o_final, 1);
     mbar_init(fin_bar, 1);
+    mbar_init(xh_empty, 4);
+    mbar_init(xh_full, 1);
     fence_barrier_init();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    mbar_arrive_expect_tx(x_full, Role::kX1Bytes + Role::kX2Bytes);
+    mbar_arrive_expect_tx(x_full, Role::kXFirst * (128 * 128) + Role::kX2Bytes);
 #pragma unroll
-    for (int bx = 0; bx < 2 * Role::kBoxes1; ++bx)
-      tma_load_3d(sX1 + bx * (64 * 128), tm_x1, x_full, (bx >> 1) * 64, x0 + (bx & 1) * 64, bh);
+    for (int bx = 0; bx < Role::kXFirst; ++bx) load_x(sX1, tm_x1, x_full, bx, 0);
     if constexpr (OUT1) {
 #pragma unroll
-      for (int bx = 0; bx < 2 * Role::kBoxes2; ++bx)
-        tma_load_3d(sX2 + bx * (64 * 128), tm_x2, x_full, (bx >> 1) * 64, x0 + (bx & 1) * 64, bh);
+      for (int bx = 0; bx < Role::kBoxes2; ++bx) load_x(sX2, tm_x2, x_full, bx, 0);
     }
   }
   if (warp == kMmaWarp) {
@@ -359,6 +385,15 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       }
       int pos_min = 0, pos_max = 0;  // query tiles: the tile's positions
       if constexpr (!KEYS) packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
+      bool x_twice = false;  // the second pass of X1 was requested
+      if constexpr (Role::TWICE) {
+        if (mbar_wait(xh_empty, 0, a.wd, kWdTmaEmpty)) {
+          x_twice = true;
+          mbar_arrive_expect_tx(xh_full, (Role::kBoxes1 - Role::kXFirst) * (128 * 128));
+#pragma unroll
+          for (int bx = Role::kXFirst; bx < Role::kBoxes1; ++bx) load_x(sX1, tm_x1, xh_full, bx, Role::kXFirst);
+        }
+      }
       // Y1 and Y2 are loaded as their slots come free, whichever is first: in one
       // fixed order a full Y2 ring would hold back the Y1 that the next scores
       // wait for.  u1 / u2: blocks loaded; behind the last block, one more Y1 slot
@@ -408,14 +443,15 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           }
         }
         const int s2 = u2 % N2;
-        if (u2 < u1 && mbar_test(&y2_empty[s2], ((uint32_t)(u2 / N2) & 1u) ^ 1u)) {
+        if (u2 < u1 && (!Role::TWICE || alias_free) && mbar_test(&y2_empty[s2], ((uint32_t)(u2 / N2) & 1u) ^ 1u)) {
           moved = true;
           const int row0 = info[u2 % NT].row0;
           mbar_arrive_expect_tx(&y2_full[s2], Role::kY2Bytes);
           uint8_t *d2 = sY2 + s2 * Role::kY2Bytes;
+          const int col0 = OUT1 ? 0 : col_part * Role::W2;  // (zeros past the head dim)
 #pragma unroll
-          for (int bx = 0; bx < Role::kBoxes2; ++bx)
-            tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], bx * 64, row0, bh);
+          for (int bx = 0; bx < Role::kY2Boxes; ++bx)
+            tma_load_3d(d2 + bx * (BN * 128), tm_y2, &y2_full[s2], col0 + bx * 64, row0, bh);
           ++u2;
         }
         if (moved) {
@@ -432,6 +468,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       }
       // drain copies still landing (only ever waits after an abort)
       mbar_wait_drain(x_full, 0, a.wd);
+      if (x_twice) mbar_wait_drain(xh_full, 0, a.wd);
       for (int v = max(u1 + last - N1, 0); v < u1; ++v)  // (not the slots used once more)
         mbar_wait_drain(&y1_full[v % N1], (uint32_t)(v / N1) & 1u, a.wd);
       for (int v = max(u2 - N2, 0); v < u2; ++v)
@@ -441,8 +478,11 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     // ========== MMA issuer: the whole warp, converged (see elect_leader) ==========
     const uint32_t leader = elect_leader();
     constexpr uint32_t kIdescS = umma_idesc_f16(kBF16, 128, BN, false, false);
-    constexpr uint32_t kIdesc1 = umma_idesc_f16(kBF16, 128, Role::D1, false, true);
-    constexpr uint32_t kIdesc2 = umma_idesc_f16(kBF16, 128, Role::D2, false, true);
+    // (the last part of a parted tile may be narrower: D1 = D2 there)
+    const int cols = Role::PARTED ? min(Role::W1, Role::D1 - col_part * Role::W1) : 0;
+    const uint32_t idesc1 = umma_idesc_f16(kBF16, 128, Role::PARTED ? cols : Role::D1, false, true);
+    const uint32_t idesc2 = umma_idesc_f16(kBF16, 128, Role::PARTED ? cols : Role::D2, false, true);
+    const uint32_t y1_cols = Role::PARTED ? col_part * (Role::W1 / 64) * (BN * 128) : 0;
     const uint32_t x1 = smem_u32(sX1), x2 = smem_u32(sX2), y1 = smem_u32(sY1), y2 = smem_u32(sY2);
     auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t code) -> bool {
       return mbar_wait_warp(bar, parity, a.wd, code);
@@ -531,7 +571,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       if constexpr (OUT2) {
         if constexpr (!OUT1)
           if (!(ok = wait(&y2_full[c2.slot], c2.parity, kWdTmaFull))) break;
-        second(cs.slot * Role::kStageCols, y2 + c2.slot * Role::kY2Bytes, Role::kOut2Col, kIdesc2, n == 0);
+        second(cs.slot * Role::kStageCols, y2 + c2.slot * Role::kY2Bytes, Role::kOut2Col, idesc2, n == 0);
         tc_commit_warp(leader, &y2_empty[c2.slot]);
       }
       bool ds_ready = false;
@@ -553,7 +593,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
                     : wait(&ds_full[st], cs.parity, kWdSoftmax);
           if (!ok) break;
         }
-        second(st * Role::kStageCols + BN, y1 + c1.slot * Role::kY1Bytes, Role::kOut1Col, kIdesc1, n == 0);
+        second(st * Role::kStageCols + BN, y1 + c1.slot * Role::kY1Bytes + y1_cols, Role::kOut1Col, idesc1, n == 0);
         tc_commit_warp(leader, &y1_empty[c1.slot]);
       }
       ++n;
@@ -602,11 +642,17 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     if constexpr (XT) {
       ok = wait(x_full, 0);
       if (Role::XT1 && group == 0) {
-        if (ok) bwd_x_to_tmem<Role::D1>(sX1, lanes + Role::kX1Col, r);
+        constexpr int kC1 = Role::D1 / 16, kFirst = Role::TWICE ? Role::kXFirst * 4 : kC1;
+        if (ok) bwd_x_to_tmem<0, kFirst>(sX1, lanes + Role::kX1Col, r);
+        if constexpr (Role::TWICE) {
+          arrive(xh_empty);
+          ok = ok && wait(xh_full, 0);
+          if (ok) bwd_x_to_tmem<kFirst, kC1>(sX1, lanes + Role::kX1Col, r);
+        }
         arrive(xt_full);
       }
       if (Role::XT2 && group == 1) {
-        if (ok) bwd_x_to_tmem<Role::D2>(sX2, lanes + Role::kX2Col, r);
+        if (ok) bwd_x_to_tmem<0, Role::D2 / 16>(sX2, lanes + Role::kX2Col, r);
         arrive(xt_full);
       }
     }
@@ -721,8 +767,8 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     ok = wait(have ? o_final : x_full, 0) && ok;
     const bool have_o = have && ok;
     const int nvalid = min(kBwdTcRows, xrows - x0);
-    auto finish = [&](int col, int d, float factor, uint8_t *stage, float *out_part) {
-      const int chunks = d / 16;
+    auto finish = [&](int col, int d, int first, int width, float factor, uint8_t *stage, float *out_part) {
+      const int chunks = min(width, d - first) / 16;
       for (int c16 = group * chunks / 2; c16 < (group + 1) * chunks / 2; ++c16) {
         float o[16];
         if (have_o) {
@@ -739,29 +785,30 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
           stage_16bit_x16(stage, r, c16, w8);
         } else if (r < nvalid && split < parts) {  // fp32 sums, [split][slab][row][d]
           float4 *dst = reinterpret_cast<float4 *>(
-              out_part + ((((long long)split * a.B * a.Hkv + bh) * xrows + x0 + r) * d + c16 * 16));
+              out_part + ((((long long)split * a.B * a.Hkv + bh) * xrows + x0 + r) * d + first + c16 * 16));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
     };
+    const int first1 = col_part * Role::W1, first2 = col_part * Role::W2;  // gradient columns
     const bool split_out = parts > 1;
     if constexpr (OUT1)
-      finish(Role::kOut1Col, Role::D1, bwd_ds_factor<kBF16>(p, gain), smem + Role::kStage1Off, split_out ? span.part1 : nullptr);
+      finish(Role::kOut1Col, Role::D1, first1, Role::W1, bwd_ds_factor<kBF16>(p, gain), smem + Role::kStage1Off, split_out ? span.part1 : nullptr);
     if constexpr (OUT2)
-      finish(Role::kOut2Col, Role::D2, bwd_dv_factor<kBF16>(), smem + Role::kStage2Off, split_out ? span.part2 : nullptr);
+      finish(Role::kOut2Col, Role::D2, first2, Role::W2, bwd_dv_factor<kBF16>(), smem + Role::kStage2Off, split_out ? span.part2 : nullptr);
     if (!split_out && split == 0) {
       fence_proxy_async_smem();
       asm volatile("bar.sync 1, %0;" ::"n"(kBwdTcSoftmaxWarps * 32) : "memory");
       // rows past the slab and columns past the head dim are clipped
       if (warp == 0 && lane == 0) {
         if constexpr (OUT1)
-          for (int bx = 0; bx < Role::kBoxes1 && bx * 64 < a.Dqk; ++bx)
-            tma_store_3d(tm_o1, smem + Role::kStage1Off + bx * (128 * 128), bx * 64, x0, bh);
+          for (int bx = 0; bx * 64 < Role::W1 && first1 + bx * 64 < a.Dqk; ++bx)
+            tma_store_3d(tm_o1, smem + Role::kStage1Off + bx * (128 * 128), first1 + bx * 64, x0, bh);
         if constexpr (OUT2)
-          for (int bx = 0; bx < Role::kBoxes2 && bx * 64 < a.Dv; ++bx)
-            tma_store_3d(tm_o2, smem + Role::kStage2Off + bx * (128 * 128), bx * 64, x0, bh);
+          for (int bx = 0; bx * 64 < Role::W2 && first2 + bx * 64 < a.Dv; ++bx)
+            tma_store_3d(tm_o2, smem + Role::kStage2Off + bx * (128 * 128), first2 + bx * 64, x0, bh);
         bulk_commit_group();
         bulk_wait_group_read0();  // the staging may go; the grid's end completes the writes
       }
@@ -789,6 +836,8 @@ constexpr uint32_t bwd_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 //             2 x  64 + 192 + X1 96 (dV)
 //   256/256   128 + 256 + X1 128    (dK)         128 + 256 + X1 128
 //             2 x  64 + 256 + X1 128 (dV)
+//   512/512   64 + 192 + X1 256     (dK)         64 + 192 + X1 256, 32-row blocks,
+//             2 x  32 + 192 + X1 256 (dV)        192 gradient columns per CTA
 template <int DQK, int DV>
 struct BwdTcRoles;
 template <int D>
@@ -827,6 +876,20 @@ struct BwdTcRoles<256, 256> {
   static constexpr uint32_t kSmem = bwd_max(KeyV::kSmemBytes, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
 };
 
+template <>
+struct BwdTcRoles<512, 512> {
+  using Key = BwdTcRole<512, 512, 32, 1, 2, 1, true, true, false, true, false, true, 192>;
+  using Query = BwdTcRole<512, 512, 32, 1, 2, 1, false, true, false, true, false, true, 192>;
+  using KeyV = BwdTcRole<512, 512, 32, 2, 5, 4, true, false, true, true, false, true, 192>;
+  static constexpr uint32_t kSmem = bwd_max(KeyV::kSmemBytes, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
+};
+
+// CTAs that share a tile, one per W gradient columns.
+template <class Role>
+__host__ __device__ constexpr int bwd_col_parts(int d) {
+  return Role::PARTED ? (d + Role::W1 - 1) / Role::W1 : 1;
+}
+
 template <bool kBF16, int DQK, int DV>
 __global__ void __launch_bounds__(kBwdTcThreads, 1)
     bwd_tc_kernel(const __grid_constant__ BwdTcMaps tm, const __grid_constant__ BwdParams p,
@@ -840,24 +903,30 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
     return;
   }
   const int slabs = p.a.B * p.a.Hkv;
-  const int key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
-  const CUtensorMap *qb = Roles::Key::BN == 64 ? &tm.q : &tm.qb, *doutb = Roles::Key::BN == 64 ? &tm.dout : &tm.doutb;
+  using Key = typename Roles::Key;
+  using KeyV = typename Roles::KeyV;
+  using Query = typename Roles::Query;
+  const int key_tiles = slabs * keys.tiles * keys.splits;
+  const int key_ctas = key_tiles * bwd_col_parts<Key>(p.a.Dqk);
+  const int row_ctas = slabs * rows.tiles * rows.splits * bwd_col_parts<Query>(p.a.Dqk);
+  const CUtensorMap *qb = Key::BN == Key::kBoxRows ? &tm.q : &tm.qb, *doutb = Key::BN == Key::kBoxRows ? &tm.dout : &tm.doutb;
   // the kind with the longest block lists first
   int id = blockIdx.x;
   if (rows_first) id = id < row_ctas ? (int)gridDim.x - row_ctas + id : id - row_ctas;
   if (id < key_ctas) {
-    bwd_tc_tile<kBF16, typename Roles::Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+    bwd_tc_tile<kBF16, Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
     return;
   }
   id -= key_ctas;
-  if constexpr (!std::is_void_v<typename Roles::KeyV>) {
-    if (id < key_ctas) {
-      bwd_tc_tile<kBF16, typename Roles::KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+  if constexpr (!std::is_void_v<KeyV>) {
+    const int v_ctas = key_tiles * bwd_col_parts<KeyV>(p.a.Dv);
+    if (id < v_ctas) {
+      bwd_tc_tile<kBF16, KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
       return;
     }
-    id -= key_ctas;
+    id -= v_ctas;
   }
-  bwd_tc_tile<kBF16, typename Roles::Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
+  bwd_tc_tile<kBF16, Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
 }
 
 // Sum of a tile's parts, where it has several, times the factor, rounded once: X rows of all

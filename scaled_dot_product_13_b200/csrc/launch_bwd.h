@@ -46,7 +46,7 @@ sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err);
 
 // Rows per block of the tcgen05 path: query rows of a key tile's block, keys of
 // a query tile's.
-constexpr int bwd_tc_key_block(int dqk, int dv) { return dqk == 192 && dv == 128 ? 48 : 64; }
-constexpr int kBwdTcQueryBlock = 64;
+constexpr int bwd_tc_key_block(int dqk, int dv) { return dqk == 512 ? 32 : dqk == 192 && dv == 128 ? 48 : 64; }
+constexpr int bwd_tc_query_block(int dqk) { return dqk == 512 ? 32 : 64; }
 
 }  // namespace sdpa

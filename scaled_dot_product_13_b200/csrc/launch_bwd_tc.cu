@@ -21,8 +21,10 @@ cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const BwdTcSpan &span,
 template <bool kBF16, int DQK, int DV>
 sdpa_status run(const BwdLaunch &ln, std::string *err) {
   using Roles = BwdTcRoles<DQK, DV>;
-  static_assert(Roles::Key::BN == bwd_tc_key_block(DQK, DV) && Roles::Query::BN == kBwdTcQueryBlock,
+  constexpr int kBox = Roles::Query::kBoxRows;
+  static_assert(Roles::Key::BN == bwd_tc_key_block(DQK, DV) && Roles::Query::BN == bwd_tc_query_block(DQK),
                 "the plan counts the kernel's blocks");
+  static_assert(Roles::Query::BN == kBox && Roles::Key::kBoxRows == kBox, "one map serves X tiles and key blocks");
   if constexpr (!std::is_void_v<typename Roles::KeyV>)
     static_assert(Roles::KeyV::BN == Roles::Key::BN, "both read the same boxes of Q and dO");
   auto kern = bwd_tc_kernel<kBF16, DQK, DV>;
@@ -36,8 +38,9 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   BwdTcSpan keys = {(pb.S + 127) / 128, pl.key_splits, pl.key_per, ln.key_parts, ln.key_part1, ln.key_part2};
   BwdTcSpan rows = {(pl.rows + 127) / 128, pl.row_splits, pl.row_per, ln.row_parts, ln.row_part, nullptr};
   const long long key_ctas = slabs * keys.tiles * keys.splits, row_ctas = slabs * rows.tiles * rows.splits;
-  const long long ctas = key_ctas * (std::is_void_v<typename Roles::KeyV> ? 1 : 2) + row_ctas;
-  const long long join_ctas = slabs * (pb.S > pl.rows ? (long long)pb.S : pl.rows) * 64 / 256;
+  long long ctas = key_ctas * bwd_col_parts<typename Roles::Key>(pb.Dqk) + row_ctas * bwd_col_parts<typename Roles::Query>(pb.Dqk);
+  if constexpr (!std::is_void_v<typename Roles::KeyV>) ctas += key_ctas * bwd_col_parts<typename Roles::KeyV>(pb.Dv);
+  const long long join_ctas = slabs * (pb.S > pl.rows ? (long long)pb.S : pl.rows) * 128 / 256;
   if (ctas > 0x7fffffffLL || join_ctas > 0x7fffffffLL) {
     *err = "problem needs more than 2^31 CTAs";
     return SDPA_ERR_UNSUPPORTED;
@@ -51,11 +54,11 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   constexpr int BK = Roles::Key::BN;
   const int R = pl.rows, S = pb.S, Dqk = pb.Dqk, Dv = pb.Dv;
   BwdTcMaps tm;
-  if (!map(&tm.q, ln.q, Dqk, R, 64) || !map(&tm.k, ln.k, Dqk, S, 64) || !map(&tm.v, ln.v, Dv, S, 64) ||
-      !map(&tm.dout, ln.dout, Dv, R, 64) || !map(&tm.dq, ln.dq, Dqk, R, 128) ||
+  if (!map(&tm.q, ln.q, Dqk, R, kBox) || !map(&tm.k, ln.k, Dqk, S, kBox) || !map(&tm.v, ln.v, Dv, S, kBox) ||
+      !map(&tm.dout, ln.dout, Dv, R, kBox) || !map(&tm.dq, ln.dq, Dqk, R, 128) ||
       !map(&tm.dk, ln.dk, Dqk, S, 128) || !map(&tm.dv, ln.dv, Dv, S, 128))
     return SDPA_ERR_CUDA;
-  if (BK == 64) {
+  if (BK == kBox) {
     tm.qb = tm.q;
     tm.doutb = tm.dout;
   } else if (!map(&tm.qb, ln.q, Dqk, R, BK) || !map(&tm.doutb, ln.dout, Dv, R, BK)) {
@@ -96,6 +99,7 @@ sdpa_status run_dtype(const BwdLaunch &ln, std::string *err) {
     case 3: return run<kBF16, 192, 128>(ln, err);
     case 4: return run<kBF16, 192, 192>(ln, err);
     case 5: return run<kBF16, 256, 256>(ln, err);
+    case 6: return run<kBF16, 512, 512>(ln, err);
   }
   *err = "internal: no tcgen05 backward instance for this head-dim pair";
   return SDPA_ERR_UNSUPPORTED;

@@ -45,8 +45,6 @@ def check(sdpa, m, path="auto", **kw):
 @pytest.mark.parametrize("Dqk,Dv", [(64, 64), (72, 72), (128, 128), (192, 128), (256, 256), (8, 8), (16, 256), (512, 512), (320, 40), (104, 96), (192, 192), (128, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_head_dims(cuda_lib, path, Dqk, Dv, dtype):
-    if path == "tc" and max(Dqk, Dv) > 256:
-        pytest.skip("the tcgen05 path is built for head dims up to 256")
     check(cuda_lib, O.make(2, 4, 2, 150, 150, Dqk, Dv, DT[dtype], seed=1, causal=True), path)
     check(cuda_lib, O.make(1, 3, 1, 77, 201, Dqk, Dv, DT[dtype], seed=2), path)
 
@@ -71,7 +69,7 @@ def test_windows(cuda_lib, path, window, L, S, g):
 
 @pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("offset", [0, 1, 40, 200, 500])
-@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("D", [64, 256, 512])
 def test_query_offset(cuda_lib, path, offset, D):
     m = O.make(1, 4, 2, 100, 300, D, D, torch.bfloat16, seed=6, causal=True, offset=offset)
     got = check(cuda_lib, m, path)
@@ -114,7 +112,7 @@ def test_many_equal_keys_in_fp16(cuda_lib, path):
 
 
 @pytest.mark.parametrize("path", PATHS)
-@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
 def test_rows_without_keys(cuda_lib, path, D):
     """lse = -inf: the row takes no part, whatever its out and dout hold."""
     m = O.make(1, 4, 2, 140, 140, D, D, torch.bfloat16, seed=14, causal=True, sinks=True, dlse=True)
@@ -151,7 +149,8 @@ def test_future_values_that_are_not_numbers(cuda_lib, path):
 
 
 @pytest.mark.parametrize("path", PATHS)
-@pytest.mark.parametrize("shape", [(2, 6, 2, 70, 90, 72, 72), (1, 8, 8, 64, 2000, 128, 128), (1, 2, 1, 300, 300, 256, 256)])
+@pytest.mark.parametrize("shape", [(2, 6, 2, 70, 90, 72, 72), (1, 8, 8, 64, 2000, 128, 128), (1, 2, 1, 300, 300, 256, 256), (1, 2, 1, 300, 300, 512, 512),
+                                   (1, 2, 1, 20, 3000, 512, 320)])
 def test_nothing_else_is_written(cuda_lib, path, shape):
     """Guard bands around every output and the workspace; the workspace's old
     contents do not matter; a second call gives the same bits."""

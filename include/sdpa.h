@@ -296,9 +296,9 @@ SDPA_API sdpa_status sdpa_forward_planned(const void *q, const void *k, const vo
  *                  written (0 for keys that no row sees)
  *   the rest       as in the forward call; opt may be NULL
  * A row whose lse is -inf contributes nothing.  The sums run in a fixed order:
- * the same call gives the same bits.  P and dS are rounded to the 16-bit type
- * (fp16: after scaling by powers of two, so that small gradients need no loss
- * scale to survive it); all sums are fp32.
+ * the same call gives the same bits.  P and dS enter their products as 16-bit
+ * values, one or the sum of two (weight_terms; fp16: after scaling by powers of
+ * two, so that small gradients need no loss scale); all sums are fp32.
  * Workspace: sdpa_backward_workspace_bytes(...) bytes, always above 0;
  * workspace NULL with workspace_bytes 0 takes it stream-ordered from the pool
  * like sdpa_forward.  Nothing in it needs clearing.
@@ -307,14 +307,6 @@ SDPA_API sdpa_status sdpa_forward_planned(const void *q, const void *k, const vo
  * or for dsinks without sinks; SDPA_ERR_RESOURCES when the workspace is too
  * small.
  */
-typedef enum {
-  SDPA_BWD_PATH_AUTO = 0,
-  SDPA_BWD_PATH_TILE = 1, /* 64-row tiles on warp-level tensor-core tiles, any
-                             head dims                                      */
-  SDPA_BWD_PATH_TC = 2    /* 128-row tiles on tcgen05 with TMEM accumulators,
-                             head dims up to 256                            */
-} sdpa_backward_path;
-
 /* Options of sdpa_backward (zero-initialise, then set what is needed). */
 typedef struct {
   int has_q_offset; /* as in sdpa_options */
@@ -323,7 +315,10 @@ typedef struct {
   float *dsinks;      /* [Hq] their gradient (needs sinks)                   */
   const float *dlse;  /* [B][Hq][L] gradient of lse, where lse was used
                          (a merge of results over disjoint key ranges)       */
-  int force_path;     /* sdpa_backward_path; 0 = the router's choice         */
+  int weight_terms;   /* 16-bit terms that P and dS enter their products as: 1,
+                         2 (their rounding no longer shows, at up to 1.4 times
+                         the products), 0 = 2 where that costs no time, for
+                         small problems, else 1                              */
 } sdpa_backward_options;
 
 SDPA_API sdpa_status sdpa_backward(const void *q, const void *k, const void *v, const void *out,
@@ -336,7 +331,7 @@ SDPA_API sdpa_status sdpa_backward(const void *q, const void *k, const void *v, 
 
 /*
  * Workspace of sdpa_backward for this problem on the current device (of its
- * options only has_q_offset, q_offset and force_path matter).  Returns 0 and
+ * options only has_q_offset, q_offset and weight_terms matter).  Returns 0 and
  * sets the last error message when the arguments are invalid.
  */
 SDPA_API size_t sdpa_backward_workspace_bytes(int B, int Hq, int Hkv, int L, int S, int Dqk,

@@ -20,7 +20,7 @@ import os
 import struct
 
 __all__ = ["forward", "forward_ws", "forward_noalloc", "forward_ex", "Options", "workspace_bytes", "plan", "device_status",
-           "backward", "backward_workspace_bytes", "BackwardOptions", "BWD_PATH_AUTO", "BWD_PATH_TILE", "BWD_PATH_TC",
+           "backward", "backward_workspace_bytes", "BackwardOptions",
            "rotary", "rotary_plan", "RotaryPlan", "ROPE_SCALINGS",
            "set_wait_limit_ns", "watchdog_selftest", "exp2_selftest", "time_next_main_kernel", "time_next_call", "load_library", "library_path",
            "SdpaError", "PATH_AUTO", "PATH_SPLITKV", "PATH_TC", "PATH_TC2", "PATH_WIDE", "PATH_TC_DUAL", "PATH_TC_KSPLIT",
@@ -31,7 +31,6 @@ _LIB: ctypes.CDLL | None = None
 
 PATH_AUTO, PATH_SPLITKV, PATH_TC, PATH_TC2, PATH_WIDE, PATH_TC_DUAL, PATH_TC_KSPLIT, PATH_TC2_LOOP = \
     0, 1, 2, 3, 4, 5, 6, 7
-BWD_PATH_AUTO, BWD_PATH_TILE, BWD_PATH_TC = 0, 1, 2
 STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTED",
           3: "SDPA_ERR_RESOURCES", 4: "SDPA_ERR_CUDA", 5: "SDPA_ERR_TIMEOUT"}
 
@@ -65,7 +64,7 @@ class BackwardOptions(ctypes.Structure):
     """Mirror of sdpa_backward_options."""
     _fields_ = [("has_q_offset", ctypes.c_int), ("q_offset", ctypes.c_int),
                 ("sinks", ctypes.c_void_p), ("dsinks", ctypes.c_void_p), ("dlse", ctypes.c_void_p),
-                ("force_path", ctypes.c_int)]
+                ("weight_terms", ctypes.c_int)]
 
 
 class RotaryConfig(ctypes.Structure):
@@ -306,13 +305,13 @@ def plan(B, Hq, Hkv, L, S, Dqk, Dv, causal=False, window_size=0, dtype="bf16",
 
 
 def backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, causal=False, window_size=0, dtype="bf16",
-                             q_offset: int | None = None, force_path: int = 0) -> int:
+                             q_offset: int | None = None, weight_terms: int = 0) -> int:
     """Workspace that ``backward`` needs for this problem on the current device."""
     lib = load_library()
     opt = BackwardOptions()
     if q_offset is not None:
         opt.has_q_offset, opt.q_offset = 1, int(q_offset)
-    opt.force_path = int(force_path)
+    opt.weight_terms = int(weight_terms)
     n = lib.sdpa_backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, int(bool(causal)), int(window_size),
                                           0 if dtype in ("bf16", "bfloat16") else 1, ctypes.byref(opt))
     if n == 0:
@@ -323,12 +322,14 @@ def backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, causal=False, window_siz
 
 def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool = False, window_size: int = 0,
              q_offset: int | None = None, sinks=None, dlse=None, dq=None, dk=None, dv=None, dsinks=None,
-             stream=None, workspace=None, force_path: int = 0):
+             stream=None, workspace=None, weight_terms: int = 0):
     """Gradients (dq, dk, dv) of ``forward_ex(q, k, v, ..., lse=lse)``, given its
     ``out`` and ``lse`` and the gradient ``dout`` of out; the other arguments as
     in that call.  ``dlse``: gradient [B, Hq, L] (float32) of lse, where it was
     used.  ``dsinks``: float32 [Hq] that receives the gradient of ``sinks``.
     ``dq`` / ``dk`` / ``dv``: contiguous tensors to write (new ones when None).
+    ``weight_terms``: 16-bit terms that P and dS enter their products as, 1 or 2
+    (0: 2 for small problems, where it costs no time).
     ``workspace``: at least ``backward_workspace_bytes`` bytes on the device,
     not used by other work until the call's kernels are done.  None: from
     torch's caching allocator on the current stream, or, with ``stream`` given,
@@ -359,14 +360,14 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
         opt.dsinks = want("dsinks", dsinks, (Hq,), f32)
     if dlse is not None:
         opt.dlse = want("dlse", dlse, rows, f32)
-    if force_path:
-        opt.force_path = int(force_path)
+    if weight_terms:
+        opt.weight_terms = int(weight_terms)
     opt = ctypes.byref(opt)
     causal, window_size = 1 if causal else 0, int(window_size)
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return backward(q, k, v, out, lse, dout, scale, causal, window_size, q_offset, sinks, dlse, dq, dk, dv,
-                            dsinks, stream, workspace, force_path)
+                            dsinks, stream, workspace, weight_terms)
     # (q, k and v are contiguous)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk

@@ -16,6 +16,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 sdpa_status refuse(sdpa_status st, const char *msg) { return set_error(st, msg); }
 
+// Up to this many pairs of row and key, P and dS enter their products as two
+// 16-bit terms: a call is bound by latency there (TWOTERM), and with
+// few pairs the rounding of single weights does not average out.
+constexpr long long kTwoTermPairs = 1 << 20;
+
 // Blocks each part of a split tile keeps at least: below that its operand
 // loads and its share of the join cost more than the parallelism gives.
 constexpr int kMinBlocksPerPart = 4;
@@ -23,65 +28,60 @@ constexpr int kMinBlocksPerPart = 4;
 // at 1.3 (the causal 192/128 case, a ragged chunk) splitting cost 6 to 18 %.
 constexpr double kSplitOver = 1.5;
 
-sdpa_status make_bwd_plan(const Problem &pb, int sms, int force_path, BwdPlan *out) {
+sdpa_status make_bwd_plan(const Problem &pb, int sms, int weight_terms, BwdPlan *out) {
   BwdPlan pl;
   memset(&pl, 0, sizeof(pl));
   const long long rows = (long long)pb.Hq / pb.Hkv * pb.L;
-  const long long kMax = 0x7fffffffLL - 1024;  // tile and block ends stay in 32 bits
-  if (rows > kMax || pb.S > kMax)
-    return refuse(SDPA_ERR_UNSUPPORTED, "more than 2^31 - 1025 packed query rows per KV head, or keys");
+  if (rows > (1 << 30) || pb.S > (1 << 30))  // tile and block ends stay in 32 bits
+    return refuse(SDPA_ERR_UNSUPPORTED, "more than 2^30 packed query rows per KV head, or keys");
   pl.rows = (int)rows;
-  if (force_path != SDPA_BWD_PATH_AUTO && force_path != SDPA_BWD_PATH_TILE && force_path != SDPA_BWD_PATH_TC)
-    return refuse(SDPA_ERR_INVALID_ARG, "unknown backward path");
+  if (weight_terms < 0 || weight_terms > 2) return refuse(SDPA_ERR_INVALID_ARG, "weight_terms must be 0, 1 or 2");
+  pl.weight_terms = weight_terms != 0                                             ? weight_terms
+                    : (double)pb.B * pb.Hq * pb.L * pb.S <= (double)kTwoTermPairs ? 2
+                                                                                  : 1;
   pl.pair = 0;
-  while (pl.pair < kNumDimPairs && (kDimPairs[pl.pair].dqk < pb.Dqk || kDimPairs[pl.pair].dv < pb.Dv)) ++pl.pair;
-  const bool tc_fits = rows < (1 << 30) && pb.S < (1 << 30);
-  if (force_path == SDPA_BWD_PATH_TC && !tc_fits)
-    return refuse(SDPA_ERR_UNSUPPORTED, "the tcgen05 backward path is built for up to 2^30 rows and keys");
-  pl.path = force_path != SDPA_BWD_PATH_AUTO ? force_path : tc_fits ? SDPA_BWD_PATH_TC : SDPA_BWD_PATH_TILE;
+  while (kDimPairs[pl.pair].dqk < pb.Dqk || kDimPairs[pl.pair].dv < pb.Dv) ++pl.pair;  // (512/512 covers all)
   pl.rpad = (pl.rows + 127) / 128 * 128;
   pl.key_splits = pl.row_splits = 1;
   const size_t slabs = (size_t)pb.B * pb.Hkv;
-  if (pl.path == SDPA_BWD_PATH_TC) {
-    const DimPair dp = kDimPairs[pl.pair];
-    const int bk = bwd_tc_key_block(dp.dqk, dp.dv), bq = bwd_tc_query_block(dp.dqk);
-    if (128 % bk != 0) pl.rpad += 128;  // 48-row blocks end up to 47 rows behind the slab
-    // Split a tile's block list where one tile would outlast the whole grid's
-    // work spread over the SMs (few tiles with long lists: few query rows over
-    // many keys, one KV head under many rows, the first keys of a causal call).
-    // Work in pairs of row and key that the mask leaves, times 4 products in a
-    // key tile, 3 in a query tile.
-    const int g = pb.Hq / pb.Hkv;
-    const double first = pb.causal ? std::min<double>(pb.S, pb.q_offset + 1.0) : pb.S;
-    const double last = pb.causal ? std::min<double>(pb.S, (double)pb.q_offset + pb.L) : pb.S;
-    double per_row = 0.5 * (first + last);  // keys that a row sees, on average
-    if (pb.window > 0) per_row = std::min<double>(per_row, pb.window);
-    const double ideal = (double)slabs * g * pb.L * per_row * 7 / sms;
-    // the longest lists: of the first keys, and of the last rows (whose tile
-    // spans all positions where it runs over the end of a head)
-    const long long seen_rows = pb.window > 0 ? std::min<long long>(pb.L, (long long)pb.window + 128) : pb.L;
-    const long long span = g > 1 && pb.L % 128 != 0 ? pb.L : std::min(pb.L, 128);
-    const long long row_keys = pb.window > 0 ? std::min<long long>(last, pb.window + span) : (long long)last;
-    const long long kb = (g * seen_rows + bk - 1) / bk, rb = (row_keys + bq - 1) / bq;
-    auto parts = [&](long long blocks, int pairs, int *per) {
-      const double over = (double)blocks * pairs * 128 / ideal;
-      int n = 1;
-      if (over > kSplitOver) n = (int)std::max(1.0, std::min(std::ceil(over), (double)(blocks / kMinBlocksPerPart)));
-      *per = (int)((blocks + n - 1) / n);
-      return n;
-    };
-    pl.key_splits = parts(kb, 4 * bk, &pl.key_per);
-    pl.row_splits = parts(rb, 3 * bq, &pl.row_per);
-    pl.rows_first = (long long)pl.row_per * bq * 3 > (long long)pl.key_per * bk * 4;
-    if (pl.key_splits > 1) {
-      pl.key_part1_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dqk * sizeof(float));
-      pl.key_part2_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dv * sizeof(float));
-    }
-    if (pl.row_splits > 1)
-      pl.row_part_bytes = align256((size_t)pl.row_splits * slabs * pl.rows * dp.dqk * sizeof(float));
-    if (pl.key_splits > 1 || pl.row_splits > 1)
-      pl.count_bytes = align256(slabs * ((pb.S + 127) / 128 + (pl.rows + 127) / 128) * sizeof(int));
+  const DimPair dp = kDimPairs[pl.pair];
+  const int bk = bwd_tc_key_block(dp.dqk, dp.dv), bq = bwd_tc_query_block(dp.dqk);
+  if (128 % bk != 0) pl.rpad += 128;  // 48-row blocks end up to 47 rows behind the slab
+  // Split a tile's block list where one tile would outlast the whole grid's
+  // work spread over the SMs (few tiles with long lists: few query rows over
+  // many keys, one KV head under many rows, the first keys of a causal call).
+  // Work in pairs of row and key that the mask leaves, times 4 products in a
+  // key tile, 3 in a query tile.
+  const int g = pb.Hq / pb.Hkv;
+  const double first = pb.causal ? std::min<double>(pb.S, pb.q_offset + 1.0) : pb.S;
+  const double last = pb.causal ? std::min<double>(pb.S, (double)pb.q_offset + pb.L) : pb.S;
+  double per_row = 0.5 * (first + last);  // keys that a row sees, on average
+  if (pb.window > 0) per_row = std::min<double>(per_row, pb.window);
+  const double ideal = (double)slabs * g * pb.L * per_row * 7 / sms;
+  // the longest lists: of the first keys, and of the last rows (whose tile
+  // spans all positions where it runs over the end of a head)
+  const long long seen_rows = pb.window > 0 ? std::min<long long>(pb.L, (long long)pb.window + 128) : pb.L;
+  const long long span = g > 1 && pb.L % 128 != 0 ? pb.L : std::min(pb.L, 128);
+  const long long row_keys = pb.window > 0 ? std::min<long long>(last, pb.window + span) : (long long)last;
+  const long long kb = (g * seen_rows + bk - 1) / bk, rb = (row_keys + bq - 1) / bq;
+  auto parts = [&](long long blocks, int pairs, int *per) {
+    const double over = (double)blocks * pairs * 128 / ideal;
+    int n = 1;
+    if (over > kSplitOver) n = (int)std::max(1.0, std::min(std::ceil(over), (double)(blocks / kMinBlocksPerPart)));
+    *per = (int)((blocks + n - 1) / n);
+    return n;
+  };
+  pl.key_splits = parts(kb, 4 * bk, &pl.key_per);
+  pl.row_splits = parts(rb, 3 * bq, &pl.row_per);
+  pl.rows_first = (long long)pl.row_per * bq * 3 > (long long)pl.key_per * bk * 4;
+  if (pl.key_splits > 1) {
+    pl.key_part1_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dqk * sizeof(float));
+    pl.key_part2_bytes = align256((size_t)pl.key_splits * slabs * pb.S * dp.dv * sizeof(float));
   }
+  if (pl.row_splits > 1)
+    pl.row_part_bytes = align256((size_t)pl.row_splits * slabs * pl.rows * dp.dqk * sizeof(float));
+  if (pl.key_splits > 1 || pl.row_splits > 1)
+    pl.count_bytes = align256(slabs * ((pb.S + 127) / 128 + (pl.rows + 127) / 128) * sizeof(int));
   pl.row_bytes = align256(slabs * pl.rpad * sizeof(float));
   pl.norm_bytes = align256(slabs * 16);
   pl.ws_bytes = 2 * pl.row_bytes + pl.norm_bytes + pl.count_bytes + pl.key_part1_bytes + pl.key_part2_bytes + pl.row_part_bytes;
@@ -122,7 +122,7 @@ extern "C" SDPA_API size_t sdpa_backward_workspace_bytes(int B, int Hq, int Hkv,
   uint64_t limit;
   if (device_info(&sms, &wd, &limit) != SDPA_OK) return 0;
   BwdPlan pl;
-  if (make_bwd_plan(pb, sms, opt ? opt->force_path : 0, &pl) != SDPA_OK) return 0;
+  if (make_bwd_plan(pb, sms, opt ? opt->weight_terms : 0, &pl) != SDPA_OK) return 0;
   return pl.ws_bytes;
 }
 
@@ -168,7 +168,7 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
   memset(&ln, 0, sizeof(ln));
   st = device_info(&ln.sms, &ln.wd_word, &ln.wd_limit_ns);
   if (st != SDPA_OK) return st;
-  st = make_bwd_plan(pb, ln.sms, opt ? opt->force_path : 0, &ln.plan);
+  st = make_bwd_plan(pb, ln.sms, opt ? opt->weight_terms : 0, &ln.plan);
   if (st != SDPA_OK) return st;
   const BwdPlan &pl = ln.plan;
   const cudaStream_t cs = (cudaStream_t)stream;
@@ -200,7 +200,7 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
 
   std::string err;
   st = launch_bwd_rows(ln, &err);
-  if (st == SDPA_OK) st = pl.path == SDPA_BWD_PATH_TC ? launch_bwd_tc(ln, &err) : launch_bwd_tile(ln, &err);
+  if (st == SDPA_OK) st = dtype == SDPA_BF16 ? launch_bwd_bf16(ln, &err) : launch_bwd_f16(ln, &err);
   if (st == SDPA_OK && dsinks) {
     bwd_sinks_kernel<<<Hq, kBwdSinksThreads, 0, cs>>>(sinks, lse, ln.ndelta, dsinks, B, Hq, Hkv, L, pl.rpad);
     cudaError_t e = cudaGetLastError();

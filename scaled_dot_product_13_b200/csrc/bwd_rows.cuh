@@ -27,13 +27,6 @@ struct BwdRowsParams {
   int v_ctas;          // ... per slab
 };
 
-template <bool kBF16>
-__device__ __forceinline__ float2 widen2(uint32_t x) {
-  if constexpr (kBF16)
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-}
-
 __device__ __forceinline__ float sum8(float x) {
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -67,7 +60,7 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
     const int r = (int)(prow - (long long)bh * p.rpad);
     const bool live = r < p.R;
     const long long row = (long long)bh * p.R + r;
-    float dot = 0.f, sq = 0.f;
+    float part[4] = {0.f, 0.f, 0.f, 0.f}, sq = 0.f;  // four short sums: less rounding than one
     if (live) {
       const uint4 *o = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.out) + row * p.Dv);
       const uint4 *d = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dout) + row * p.Dv);
@@ -77,13 +70,13 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
         const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 a = widen2<kBF16>(ow[i]), b = widen2<kBF16>(dw[i]);
-          dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+          const float2 a = unpack2<kBF16>(ow[i]), b = unpack2<kBF16>(dw[i]);
+          part[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, part[i]));
           if constexpr (!kBF16) sq = fmaf(b.x, b.x, fmaf(b.y, b.y, sq));
         }
       }
     }
-    dot = sum8(dot);
+    const float dot = sum8((part[0] + part[1]) + (part[2] + part[3]));
     float dl = 0.f;
     if (live && p.dlse != nullptr) dl = p.dlse[row];
     if (sub == 0) {
@@ -108,7 +101,7 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 a = widen2<kBF16>(w[i]);
+          const float2 a = unpack2<kBF16>(w[i]);
           sq = fmaf(a.x, a.x, fmaf(a.y, a.y, sq));
         }
       }
@@ -132,7 +125,7 @@ __global__ void __launch_bounds__(kBwdSinksThreads)
     const float *ls = lse + ((long long)b * Hq + h) * L;
     const float *nd = ndelta + (long long)(b * Hkv + h / g) * rpad + (long long)(h % g) * L;
     for (int i = threadIdx.x; i < L; i += kBwdSinksThreads)
-      if (ls[i] != -INFINITY) sum += (double)(expf(sink - ls[i]) * nd[i]);
+      if (ls[i] != -INFINITY) sum += exp((double)sink - ls[i]) * nd[i];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -1,5 +1,4 @@
-// Backward pass on tcgen05 tensor cores with TMEM accumulators (sm_100a),
-// head dims up to 256.
+// Backward pass on tcgen05 tensor cores with TMEM accumulators (sm_100a).
 //
 // One CTA owns a tile of 128 X rows and walks over blocks of BN Y rows:
 //   key tiles    X = keys:  X1 = K, X2 = V,  Y1 = Q, Y2 = dO:  dK and/or dV
@@ -32,6 +31,10 @@
 //            out1_n, dP_{n+ST}  after dS_n
 //        One warp's MMAs run in issue order, so S_{n+ST} may overwrite P_n once
 //        out2_n is issued.
+//
+// With TWO, P and dS go in as two terms, the 16-bit value and the 16-bit value of
+// what its rounding left, in the two halves of the columns they came from: twice
+// the second products, and the gradients' own rounding is the only one that shows.
 //
 // What bounds it.  P_n -> out2_n, S_{n+1} -> P_{n+1} is a chain through one score
 // buffer: with ST = 1 it took 4300 cycles per 128 x 128 pairs of a key tile at
@@ -227,6 +230,13 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, float *v) {
   }
 }
 
+// What rounding the pair (a, b) to 16 bits, to w, left of it, rounded itself.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t w) {
+  const float2 r = unpack2<kBF16>(w);
+  return pack2<kBF16>(a - r.x, b - r.y);
+}
+
 // X (boxes of 128 rows x 64 columns, 128-byte swizzled) to TMEM as the A operand of
 // a first product: 16-bit pairs, a row per lane.  Four warps, one row per thread.
 // Columns [16 C0, 16 C1); x holds the boxes from column 16 C0 on.
@@ -250,7 +260,7 @@ __device__ __forceinline__ void bwd_x_to_tmem(const uint8_t *x, uint32_t taddr, 
   tmem_wait_st();
 }
 
-template <bool kBF16, class Role>
+template <bool kBF16, bool TWO, class Role>
 __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMap *tm_x1,
                                             const CUtensorMap *tm_x2, const CUtensorMap *tm_y1,
                                             const CUtensorMap *tm_y2, const CUtensorMap *tm_o1,
@@ -509,11 +519,13 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       tc_fence_after();
       const uint64_t b0 = umma_desc_sw128_mn(y, BN * 128, 1024);
 #pragma unroll
-      for (int ks = 0; ks < BN / 16; ++ks) {
-        const int part = ks / (kH / 16);
-        tc_mma_ts_warp(leader, tmem + out, tmem + wcol + part * kH + (ks - part * (kH / 16)) * 8,
-                       umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 ? 0u : 1u);
-      }
+      for (int term = 0; term < (TWO ? 2 : 1); ++term)
+#pragma unroll
+        for (int ks = 0; ks < BN / 16; ++ks) {
+          const int part = ks / (kH / 16);
+          tc_mma_ts_warp(leader, tmem + out, tmem + wcol + part * kH + term * (kH / 2) + (ks - part * (kH / 16)) * 8,
+                         umma_desc_advance(b0, ks * 2048), idesc, fresh && ks == 0 && term == 0 ? 0u : 1u);
+        }
     };
     bool ok = wait(x_full, 0, kWdTmaFull);
     if (XT) ok = ok && wait(xt_full, 0, kWdSoftmax);
@@ -723,6 +735,11 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
 #pragma unroll
           for (int e = 0; e < 8; ++e) pk[e] = pack2<kBF16>(w[i + 2 * e], w[i + 2 * e + 1]);
           tmem_st_u8x(t_s + i / 2, pk);
+          if constexpr (TWO) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pk[e] = rest2<kBF16>(w[i + 2 * e], w[i + 2 * e + 1], pk[e]);
+            tmem_st_u8x(t_s + kH / 2 + i / 2, pk);
+          }
         }
         tmem_wait_st();
         arrive(&p_full[st]);
@@ -740,7 +757,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         }
 #pragma unroll
         for (int j = 0; j < kH; j += 16) {
-          uint32_t pk[8];
+          uint32_t pk[8], lo[8];
 #pragma unroll
           for (int i = j; i < j + 16; i += 4) {
             float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
@@ -752,9 +769,11 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
               if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
               t = mul2(t, make_float2(w[i + e], w[i + e + 1]));
               pk[(i - j + e) / 2] = pack2<kBF16>(t.x, t.y);
+              if constexpr (TWO) lo[(i - j + e) / 2] = rest2<kBF16>(t.x, t.y, pk[(i - j + e) / 2]);
             }
           }
           tmem_st_u8x(t_dp + j / 2, pk);
+          if constexpr (TWO) tmem_st_u8x(t_dp + kH / 2 + j / 2, lo);
         }
         tmem_wait_st();
         arrive(&ds_full[st]);
@@ -890,7 +909,7 @@ __host__ __device__ constexpr int bwd_col_parts(int d) {
   return Role::PARTED ? (d + Role::W1 - 1) / Role::W1 : 1;
 }
 
-template <bool kBF16, int DQK, int DV>
+template <bool kBF16, bool TWO, int DQK, int DV>
 __global__ void __launch_bounds__(kBwdTcThreads, 1)
     bwd_tc_kernel(const __grid_constant__ BwdTcMaps tm, const __grid_constant__ BwdParams p,
                   const __grid_constant__ BwdTcSpan keys, const __grid_constant__ BwdTcSpan rows,
@@ -914,19 +933,19 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
   int id = blockIdx.x;
   if (rows_first) id = id < row_ctas ? (int)gridDim.x - row_ctas + id : id - row_ctas;
   if (id < key_ctas) {
-    bwd_tc_tile<kBF16, Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+    bwd_tc_tile<kBF16, TWO, Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
     return;
   }
   id -= key_ctas;
   if constexpr (!std::is_void_v<KeyV>) {
     const int v_ctas = key_tiles * bwd_col_parts<KeyV>(p.a.Dv);
     if (id < v_ctas) {
-      bwd_tc_tile<kBF16, KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+      bwd_tc_tile<kBF16, TWO, KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
       return;
     }
     id -= v_ctas;
   }
-  bwd_tc_tile<kBF16, Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
+  bwd_tc_tile<kBF16, TWO, Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
 }
 
 // Sum of a tile's parts, where it has several, times the factor, rounded once: X rows of all

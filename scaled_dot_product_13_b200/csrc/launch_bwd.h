@@ -8,10 +8,10 @@ namespace sdpa {
 struct BwdParams;
 
 struct BwdPlan {
-  int path;   // an sdpa_backward_path value other than AUTO
+  int weight_terms;  // 16-bit terms of P and dS: 1 or 2
   int rows;   // packed query rows per (batch, KV head)
   int rpad;   // ... rounded up so that every tile and block stays inside
-  int pair;   // tcgen05 path: index into kDimPairs
+  int pair;   // index into kDimPairs
   int key_splits, row_splits;  // parts of the longest block list of a key / query tile
   int key_per, row_per;        // blocks of a part
   int rows_first;              // the query tiles have the longer lists: first in the grid
@@ -37,14 +37,14 @@ struct BwdLaunch {
   cudaStream_t stream;
 };
 
-// Kernel parameters common to the paths.
+// Kernel parameters.
 void fill_bwd_params(const BwdLaunch &ln, BwdParams *p);
 
 sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err);
-sdpa_status launch_bwd_tile(const BwdLaunch &ln, std::string *err);
-sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err);
+sdpa_status launch_bwd_bf16(const BwdLaunch &ln, std::string *err);
+sdpa_status launch_bwd_f16(const BwdLaunch &ln, std::string *err);
 
-// Rows per block of the tcgen05 path: query rows of a key tile's block, keys of
+// Rows per block: query rows of a key tile's block, keys of
 // a query tile's.
 constexpr int bwd_tc_key_block(int dqk, int dv) { return dqk == 512 ? 32 : dqk == 192 && dv == 128 ? 48 : 64; }
 constexpr int bwd_tc_query_block(int dqk) { return dqk == 512 ? 32 : 64; }

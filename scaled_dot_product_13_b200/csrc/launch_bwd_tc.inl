@@ -1,4 +1,5 @@
-// Launch unit of the tcgen05 backward kernel and its join.
+// Launches of the tcgen05 backward kernel and its join; included by one unit per
+// type.
 #include "bwd_tc.cuh"
 #include "launch_bwd.h"
 
@@ -18,7 +19,7 @@ cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const BwdTcSpan &span,
                             span.tiles, rows, rows_per_slab, d, dpad, is_dv);
 }
 
-template <bool kBF16, int DQK, int DV>
+template <bool kBF16, bool TWO, int DQK, int DV>
 sdpa_status run(const BwdLaunch &ln, std::string *err) {
   using Roles = BwdTcRoles<DQK, DV>;
   constexpr int kBox = Roles::Query::kBoxRows;
@@ -27,7 +28,7 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   static_assert(Roles::Query::BN == kBox && Roles::Key::kBoxRows == kBox, "one map serves X tiles and key blocks");
   if constexpr (!std::is_void_v<typename Roles::KeyV>)
     static_assert(Roles::KeyV::BN == Roles::Key::BN, "both read the same boxes of Q and dO");
-  auto kern = bwd_tc_kernel<kBF16, DQK, DV>;
+  auto kern = bwd_tc_kernel<kBF16, TWO, DQK, DV>;
   sdpa_status st = prepare_kernel((const void *)kern, kBwdTcThreads, Roles::kSmem, "bwd_tc_kernel", err);
   if (st != SDPA_OK) return st;
   const Problem &pb = ln.pb;
@@ -90,25 +91,33 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   return SDPA_OK;
 }
 
-template <bool kBF16>
-sdpa_status run_dtype(const BwdLaunch &ln, std::string *err) {
+template <bool kBF16, bool TWO>
+sdpa_status run_pair(const BwdLaunch &ln, std::string *err) {
   switch (ln.plan.pair) {
-    case 0: return run<kBF16, 64, 64>(ln, err);
-    case 1: return run<kBF16, 80, 80>(ln, err);
-    case 2: return run<kBF16, 128, 128>(ln, err);
-    case 3: return run<kBF16, 192, 128>(ln, err);
-    case 4: return run<kBF16, 192, 192>(ln, err);
-    case 5: return run<kBF16, 256, 256>(ln, err);
-    case 6: return run<kBF16, 512, 512>(ln, err);
+    case 0: return run<kBF16, TWO, 64, 64>(ln, err);
+    case 1: return run<kBF16, TWO, 80, 80>(ln, err);
+    case 2: return run<kBF16, TWO, 128, 128>(ln, err);
+    case 3: return run<kBF16, TWO, 192, 128>(ln, err);
+    case 4: return run<kBF16, TWO, 192, 192>(ln, err);
+    case 5: return run<kBF16, TWO, 256, 256>(ln, err);
+    case 6: return run<kBF16, TWO, 512, 512>(ln, err);
   }
   *err = "internal: no tcgen05 backward instance for this head-dim pair";
   return SDPA_ERR_UNSUPPORTED;
 }
 
+template <bool kBF16>
+sdpa_status run_dtype(const BwdLaunch &ln, std::string *err) {
+  return ln.plan.weight_terms == 2 ? run_pair<kBF16, true>(ln, err) : run_pair<kBF16, false>(ln, err);
+}
+
 }  // namespace
 
-sdpa_status launch_bwd_tc(const BwdLaunch &ln, std::string *err) {
-  return ln.pb.dtype == SDPA_BF16 ? run_dtype<true>(ln, err) : run_dtype<false>(ln, err);
-}
+// (the bf16 and fp16 instances are compiled in two units, to build in parallel)
+#if SDPA_BWD_BF16
+sdpa_status launch_bwd_bf16(const BwdLaunch &ln, std::string *err) { return run_dtype<true>(ln, err); }
+#else
+sdpa_status launch_bwd_f16(const BwdLaunch &ln, std::string *err) { return run_dtype<false>(ln, err); }
+#endif
 
 }  // namespace sdpa

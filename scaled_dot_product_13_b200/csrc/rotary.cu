@@ -71,13 +71,6 @@ struct Pack<4> { using type = uint2; };
 template <>
 struct Pack<8> { using type = uint4; };
 
-// Words of two 16-bit elements (one for V = 1) to fp32 and back.
-template <bool kBF16>
-__device__ __forceinline__ float2 widen(uint32_t w) {
-  if constexpr (kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
 template <int V>
 union Elems {
   typename Pack<V>::type v;
@@ -156,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
         float x[2 * V], y[2 * V];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float2 f = widen<kBF16>(a[u].w[i]), g = widen<kBF16>(c[u].w[i]);
+          const float2 f = unpack2<kBF16>(a[u].w[i]), g = unpack2<kBF16>(c[u].w[i]);
           x[2 * i] = f.x;
           if constexpr (V > 1) x[2 * i + 1] = f.y;
           x[V + 2 * i] = g.x;

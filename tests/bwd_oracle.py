@@ -2,18 +2,19 @@
 the results to 16 bits may be from it (test infrastructure).
 
 ``gradients`` is the formula, materialised.  ``bounds`` carries the roundings
-through it, element by element, with u = half a step of the 16-bit type and
-e = 2^-24:
+through it, element by element, with u = half a step of the 16-bit type, e =
+2^-24, and v = u where P and dS enter their products as one 16-bit value, u^2
+where as two (the second holds what the first's rounding left, to u of it):
 
   scores   s = scale q.k: a sum of Dqk products in fp32, off by at most
            (Dqk + 4) e sum |q k| scale; lse is an fp32 input, its product with
            log2(e) and the exponential add 2^-22 (1 + |lse| + |s|): together
            dP/P <= es
-  P        u, and (fp16) half a subnormal step of the scaled value, 2^-39
-  dV       sum over rows of (u + es) P |dO| + 2^-39 |dO|, fp32 sums n e, one
+  P        v, and (fp16) half a subnormal step of the scaled value, 2^-39
+  dV       sum over rows of (v + es) P |dO| + 2^-39 |dO|, fp32 sums n e, one
            rounding u |dV| of the result (fp16: 2^-25 below its normal range)
   dP-delta two sums of Dv products: (Dv + 4) e (sum |dO V| + sum |dO O| + |dlse|)
-  dS       P ((u + es) |dP - delta| + that), and (fp16) 2^-39 of the bound that
+  dS       P ((v + es) |dP - delta| + that), and (fp16) 2^-39 of the bound that
            its scale is taken from
   dQ, dK   those through the last product, its fp32 sums, one rounding
 """
@@ -47,12 +48,13 @@ def forward(q, k, v, scale, causal=False, window=0, offset=None, sinks=None):
     return torch.exp(s - lse[..., None]) @ v.repeat_interleave(g, 1), lse
 
 
-def gradients(q, k, v, out, lse, dout, scale, causal=False, window=0, offset=None, sinks=None, dlse=None):
+def gradients(q, k, v, out, lse, dout, scale, causal=False, window=0, offset=None, sinks=None, dlse=None, terms=1):
     """{"dq", "dk", "dv", "dsinks"} in 64 bits, and their bounds, given the
     forward pass's (rounded) out and lse."""
     dt = q.dtype
     u = U[dt]
     half = dt == torch.float16
+    uv = u ** terms
     B, Hq, L, Dqk = q.shape
     Hkv, S, Dv = k.shape[1], k.shape[2], v.shape[3]
     g = Hq // Hkv
@@ -77,10 +79,10 @@ def gradients(q, k, v, out, lse, dout, scale, causal=False, window=0, offset=Non
 
     fl = torch.where(torch.isinf(lse), 0.0, lse.abs())[..., None]
     es = (Dqk + 4) * E * abs(scale) * (q.abs() @ kT.abs()) + 2.0 ** -22 * (1 + fl + s.abs())
-    ep = torch.where(seen, p * (u + es) + (2.0 ** -39 if half else 0.0), 0.0)
+    ep = torch.where(seen, p * (uv + es) + (2.0 ** -39 if half else 0.0), 0.0)
     et = (Dv + 4) * E * (do.abs() @ vT.abs() + (do * out).abs().sum(-1, keepdim=True) + dl.abs()[..., None])
     low = 2.0 ** -39 * (2 * do.norm(dim=-1).amax() * v.norm(dim=-1).amax() + dl.abs().amax()) if half else 0.0
-    eds = torch.where(seen, p * ((u + es) * t.abs() + et) * (1 + 2 * u) + low, 0.0)
+    eds = torch.where(seen, p * ((uv + es) * t.abs() + et) * (1 + 2 * u) + low, 0.0)
     sub = 2.0 ** -25 if half else 0.0
 
     def final(name, err, size, n):  # through the last product

@@ -8,15 +8,14 @@ from tests import bwd_oracle as O
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
-PATHS = ["tile", "tc"]
+TERMS = [1, 2]  # 16-bit terms of P and dS; 0, the choice by size, is 2 up to 2^20 pairs
 
 
-def run(sdpa, m, path="auto", **kw):
+def run(sdpa, m, terms=0, **kw):
     c = {n: (m[n].cuda() if m[n] is not None else None) for n in ("q", "k", "v", "out", "lse", "dout", "sinks", "dlse")}
     dsinks = torch.full_like(c["sinks"], float("nan")) if c["sinks"] is not None else None
-    force = {"auto": 0, "tile": sdpa.BWD_PATH_TILE, "tc": sdpa.BWD_PATH_TC}[path]
     args = dict(scale=m["scale"], causal=m["causal"], window_size=m["window"], q_offset=m["offset"], sinks=c["sinks"],
-                dlse=c["dlse"], dsinks=dsinks, force_path=force)
+                dlse=c["dlse"], dsinks=dsinks, weight_terms=terms)
     args.update(kw)
     dq, dk, dv = sdpa.backward(c["q"], c["k"], c["v"], c["out"], c["lse"], c["dout"], **args)
     got = {"dq": dq, "dk": dk, "dv": dv}
@@ -25,10 +24,11 @@ def run(sdpa, m, path="auto", **kw):
     return got
 
 
-def check(sdpa, m, path="auto", **kw):
-    got = run(sdpa, m, path, **kw)
+def check(sdpa, m, terms=0, **kw):
+    got = run(sdpa, m, terms, **kw)
     sdpa.device_status(clear=True)
-    want, tol = O.gradients(**m)
+    pairs = m["q"].shape[0] * m["q"].shape[1] * m["q"].shape[2] * m["k"].shape[2]
+    want, tol = O.gradients(**m, terms=terms or (2 if pairs <= 1 << 20 else 1))
     for n in want:
         err = (got[n].double().cpu() - want[n]).abs()
         assert torch.isfinite(got[n].float()).all(), n
@@ -41,117 +41,117 @@ def check(sdpa, m, path="auto", **kw):
     return got
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("Dqk,Dv", [(64, 64), (72, 72), (128, 128), (192, 128), (256, 256), (8, 8), (16, 256), (512, 512), (320, 40), (104, 96), (192, 192), (128, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_head_dims(cuda_lib, path, Dqk, Dv, dtype):
-    check(cuda_lib, O.make(2, 4, 2, 150, 150, Dqk, Dv, DT[dtype], seed=1, causal=True), path)
-    check(cuda_lib, O.make(1, 3, 1, 77, 201, Dqk, Dv, DT[dtype], seed=2), path)
+def test_head_dims(cuda_lib, terms, Dqk, Dv, dtype):
+    check(cuda_lib, O.make(2, 4, 2, 150, 150, Dqk, Dv, DT[dtype], seed=1, causal=True), terms)
+    check(cuda_lib, O.make(1, 3, 1, 77, 201, Dqk, Dv, DT[dtype], seed=2), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("L,S", [(1, 1), (1, 2), (1, 64), (1, 1000), (2, 129), (31, 33), (64, 64), (65, 63), (127, 128), (128, 127),
                                  (129, 257), (300, 20), (383, 385), (600, 1)])
 @pytest.mark.parametrize("g", [1, 5, 8])
-def test_lengths(cuda_lib, path, L, S, g):
-    check(cuda_lib, O.make(2, 2 * g, 2, L, S, 64, 64, torch.bfloat16, seed=L + S), path)
+def test_lengths(cuda_lib, terms, L, S, g):
+    check(cuda_lib, O.make(2, 2 * g, 2, L, S, 64, 64, torch.bfloat16, seed=L + S), terms)
     if L <= S:
-        check(cuda_lib, O.make(1, 2 * g, 2, L, S, 128, 128, torch.float16, seed=L + S, causal=True), path)
+        check(cuda_lib, O.make(1, 2 * g, 2, L, S, 128, 128, torch.float16, seed=L + S, causal=True), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 200, 1000])
 @pytest.mark.parametrize("L,S,g", [(300, 300, 2), (33, 400, 4), (257, 700, 1)])
-def test_windows(cuda_lib, path, window, L, S, g):
-    check(cuda_lib, O.make(1, 2 * g, 2, L, S, 64, 64, torch.bfloat16, seed=4, causal=True, window=window), path)
-    check(cuda_lib, O.make(1, 2 * g, 2, L, S, 192, 128, torch.float16, seed=5, causal=True, window=window), path)
+def test_windows(cuda_lib, terms, window, L, S, g):
+    check(cuda_lib, O.make(1, 2 * g, 2, L, S, 64, 64, torch.bfloat16, seed=4, causal=True, window=window), terms)
+    check(cuda_lib, O.make(1, 2 * g, 2, L, S, 192, 128, torch.float16, seed=5, causal=True, window=window), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("offset", [0, 1, 40, 200, 500])
 @pytest.mark.parametrize("D", [64, 256, 512])
-def test_query_offset(cuda_lib, path, offset, D):
+def test_query_offset(cuda_lib, terms, offset, D):
     m = O.make(1, 4, 2, 100, 300, D, D, torch.bfloat16, seed=6, causal=True, offset=offset)
-    got = check(cuda_lib, m, path)
+    got = check(cuda_lib, m, terms)
     unseen = offset + 100
     if unseen < 300:  # keys behind the last row: exactly no gradient
         assert (got["dk"][:, :, unseen:] == 0).all() and (got["dv"][:, :, unseen:] == 0).all()
-    check(cuda_lib, O.make(1, 4, 2, 100, 300, D, D, torch.float16, seed=7, causal=True, offset=min(offset, 250), window=60), path)
+    check(cuda_lib, O.make(1, 4, 2, 100, 300, D, D, torch.float16, seed=7, causal=True, offset=min(offset, 250), window=60), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_sinks_and_lse_gradient(cuda_lib, path, dtype):
-    check(cuda_lib, O.make(2, 6, 2, 130, 190, 64, 64, DT[dtype], seed=8, causal=True, sinks=True), path)
-    check(cuda_lib, O.make(2, 6, 2, 130, 190, 128, 64, DT[dtype], seed=9, dlse=True), path)
-    check(cuda_lib, O.make(3, 6, 3, 1, 50, 64, 64, DT[dtype], seed=10, sinks=True, dlse=True), path)
+def test_sinks_and_lse_gradient(cuda_lib, terms, dtype):
+    check(cuda_lib, O.make(2, 6, 2, 130, 190, 64, 64, DT[dtype], seed=8, causal=True, sinks=True), terms)
+    check(cuda_lib, O.make(2, 6, 2, 130, 190, 128, 64, DT[dtype], seed=9, dlse=True), terms)
+    check(cuda_lib, O.make(3, 6, 3, 1, 50, 64, 64, DT[dtype], seed=10, sinks=True, dlse=True), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("scale", [0.0, -0.2, 0.01, 1.0])
-def test_scales(cuda_lib, path, scale):
-    check(cuda_lib, O.make(1, 4, 2, 90, 140, 64, 64, torch.bfloat16, seed=11, scale=scale, causal=True), path)
+def test_scales(cuda_lib, terms, scale):
+    check(cuda_lib, O.make(1, 4, 2, 90, 140, 64, 64, torch.bfloat16, seed=11, scale=scale, causal=True), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("dout_scale,v_scale", [(2.0 ** -12, 1.0), (2.0 ** 6, 1.0), (1.0, 200.0), (2.0 ** -12, 200.0)])
-def test_fp16_ranges(cuda_lib, path, dout_scale, v_scale):
+def test_fp16_ranges(cuda_lib, terms, dout_scale, v_scale):
     """fp16's dS neither overflows nor drowns, whatever the gradient's scale
     (the results themselves must stay in fp16's range)."""
-    check(cuda_lib, O.make(1, 4, 2, 96, 500, 64, 64, torch.float16, seed=12, dout_scale=dout_scale, v_scale=v_scale), path)
+    check(cuda_lib, O.make(1, 4, 2, 96, 500, 64, 64, torch.float16, seed=12, dout_scale=dout_scale, v_scale=v_scale), terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
-def test_many_equal_keys_in_fp16(cuda_lib, path):
+@pytest.mark.parametrize("terms", TERMS)
+def test_many_equal_keys_in_fp16(cuda_lib, terms):
     """Weights of 1/6000, below fp16's normal range without their scale."""
     m = O.make(1, 1, 1, 40, 6000, 64, 64, torch.float16, seed=13)
     m["q"] = m["q"] * 0
     out, lse = O.forward(m["q"], m["k"], m["v"], m["scale"])
     m["out"], m["lse"] = out.half(), lse.float()
-    check(cuda_lib, m, path)
+    check(cuda_lib, m, terms)
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-def test_rows_without_keys(cuda_lib, path, D):
+def test_rows_without_keys(cuda_lib, terms, D):
     """lse = -inf: the row takes no part, whatever its out and dout hold."""
     m = O.make(1, 4, 2, 140, 140, D, D, torch.bfloat16, seed=14, causal=True, sinks=True, dlse=True)
     m["lse"][0, 1, 5:40] = -torch.inf
     m["lse"][0, 3, 139] = -torch.inf
-    got = check(cuda_lib, m, path)
+    got = check(cuda_lib, m, terms)
     assert (got["dq"][0, 1, 5:40] == 0).all() and (got["dq"][0, 3, 139] == 0).all()
 
 
-@pytest.mark.parametrize("path", PATHS)
-def test_not_a_number_stays_in_its_slab(cuda_lib, path):
+@pytest.mark.parametrize("terms", TERMS)
+def test_not_a_number_stays_in_its_slab(cuda_lib, terms):
     m = O.make(2, 4, 2, 100, 130, 64, 64, torch.float16, seed=15)
-    clean = run(cuda_lib, m, path)
+    clean = run(cuda_lib, m, terms)
     m["dout"][0, 1, 50, 3] = float("nan")  # head 1 reads KV head 0
     m["v"][1, 1, 129, 0] = float("inf")
-    got = run(cuda_lib, m, path)
+    got = run(cuda_lib, m, terms)
     for n, heads in (("dq", [(0, 2), (0, 3), (1, 0), (1, 1)]), ("dk", [(0, 1), (1, 0)]), ("dv", [(0, 1), (1, 0)])):
         for b, h in heads:
             assert torch.equal(got[n][b, h], clean[n][b, h]), n
     assert got["dq"][0, 1, 50].isnan().all()
 
 
-@pytest.mark.parametrize("path", PATHS)
-def test_future_values_that_are_not_numbers(cuda_lib, path):
+@pytest.mark.parametrize("terms", TERMS)
+def test_future_values_that_are_not_numbers(cuda_lib, terms):
     """Keys that the causal mask hides from every row of a whole block do not
     reach it: their blocks are skipped."""
     m = O.make(1, 2, 2, 100, 400, 64, 64, torch.bfloat16, seed=16, causal=True, offset=0)
-    clean = run(cuda_lib, m, path)
+    clean = run(cuda_lib, m, terms)
     m["k"][:, :, 256:] = float("nan")
     m["v"][:, :, 256:] = float("inf")
-    got = run(cuda_lib, m, path)
+    got = run(cuda_lib, m, terms)
     assert torch.equal(got["dq"], clean["dq"])
     assert torch.equal(got["dk"][:, :, :256], clean["dk"][:, :, :256]) and torch.equal(got["dv"][:, :, :256], clean["dv"][:, :, :256])
 
 
-@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("terms", TERMS)
 @pytest.mark.parametrize("shape", [(2, 6, 2, 70, 90, 72, 72), (1, 8, 8, 64, 2000, 128, 128), (1, 2, 1, 300, 300, 256, 256), (1, 2, 1, 300, 300, 512, 512),
                                    (1, 2, 1, 20, 3000, 512, 320)])
-def test_nothing_else_is_written(cuda_lib, path, shape):
+def test_nothing_else_is_written(cuda_lib, terms, shape):
     """Guard bands around every output and the workspace; the workspace's old
     contents do not matter; a second call gives the same bits."""
     m = O.make(*shape, torch.float16, seed=17, sinks=True)
@@ -160,10 +160,9 @@ def test_nothing_else_is_written(cuda_lib, path, shape):
         bufs[n] = torch.full((like.numel() + 2 * pad,), 1234.0, dtype=like.dtype, device="cuda")
         outs[n] = bufs[n][pad:pad + like.numel()].view(like.shape)
     B, Hq, Hkv, L, S, Dqk, Dv = shape
-    force = {"auto": 0, "tile": cuda_lib.BWD_PATH_TILE, "tc": cuda_lib.BWD_PATH_TC}[path]
-    need = cuda_lib.backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, dtype="f16", force_path=force)
+    need = cuda_lib.backward_workspace_bytes(B, Hq, Hkv, L, S, Dqk, Dv, dtype="f16", weight_terms=terms)
     ws = torch.full((need + 2 * pad,), 255, dtype=torch.uint8, device="cuda")
-    first = {n: t.clone() for n, t in run(cuda_lib, m, path, workspace=ws[pad:pad + need], **outs).items()}
+    first = {n: t.clone() for n, t in run(cuda_lib, m, terms, workspace=ws[pad:pad + need], **outs).items()}
     for n, b in bufs.items():
         assert (b[:pad] == 1234.0).all() and (b[-pad:] == 1234.0).all(), n
         assert torch.isfinite(outs[n].float()).all()
@@ -171,22 +170,21 @@ def test_nothing_else_is_written(cuda_lib, path, shape):
     ws.fill_(127)
     for t in outs.values():
         t.fill_(7)
-    again = run(cuda_lib, m, path, workspace=ws[pad:pad + need], **outs)
+    again = run(cuda_lib, m, terms, workspace=ws[pad:pad + need], **outs)
     for n in first:
         assert torch.equal(first[n], again[n]), n
     with pytest.raises(cuda_lib.SdpaError) as ei:
-        run(cuda_lib, m, path, workspace=ws[pad:pad + need - 1][:need - 16], **outs)
+        run(cuda_lib, m, terms, workspace=ws[pad:pad + need - 1][:need - 16], **outs)
     assert ei.value.status == 3
 
 
-@pytest.mark.parametrize("path", PATHS)
-def test_streams_and_graphs(cuda_lib, path):
+@pytest.mark.parametrize("terms", TERMS)
+def test_streams_and_graphs(cuda_lib, terms):
     m = O.make(1, 8, 2, 200, 200, 128, 128, torch.bfloat16, seed=18, causal=True)
-    want = run(cuda_lib, m, path)
+    want = run(cuda_lib, m, terms)
     c = {n: m[n].cuda() for n in ("q", "k", "v", "out", "lse", "dout")}
-    force = {"auto": 0, "tile": cuda_lib.BWD_PATH_TILE, "tc": cuda_lib.BWD_PATH_TC}[path]
     args = [c[n] for n in ("q", "k", "v", "out", "lse", "dout")]
-    kw = dict(scale=m["scale"], causal=True, force_path=force)
+    kw = dict(scale=m["scale"], causal=True, weight_terms=terms)
 
     def empty():
         return {n: torch.zeros_like(t) for n, t in want.items()}
@@ -216,20 +214,46 @@ def test_streams_and_graphs(cuda_lib, path):
     assert torch.equal(graphs[0][1]["dv"], want["dv"] * 0.5)
 
 
-def test_paths_agree_and_auto_takes_them(cuda_lib):
-    m = O.make(1, 8, 2, 400, 400, 128, 128, torch.bfloat16, seed=19, causal=True)
-    outs = [run(cuda_lib, m, p) for p in PATHS + ["auto"]]
-    for o in outs[1:]:
-        for n in o:  # roundings of P and dS may differ by fp32's order
-            d = (o[n].double() - outs[0][n].double()).norm() / outs[0][n].double().norm()
-            assert d <= 2.0 ** -7
+def test_terms_by_size(cuda_lib):
+    """The choice by size: two terms up to 2^20 pairs, one above, and what each gives."""
+    for L, chosen in ((512, 2), (513, 1)):  # 4 heads
+        m = O.make(1, 4, 2, L, L, 64, 64, torch.bfloat16, seed=19, causal=True)
+        auto, one, two = (run(cuda_lib, m, t) for t in (0, 1, 2))
+        for n in auto:
+            assert torch.equal(auto[n], (one, two)[chosen - 1][n])
+            assert not torch.equal(one[n], two[n])
 
 
-def test_unknown_path_is_refused(cuda_lib):
+def test_two_terms_leave_one_rounding(cuda_lib):
+    """With two terms each result is the nearest 16-bit value, but where the fp32
+    sums before it are within their own error of a tie: 2^-10 of them here (sums
+    of 300 terms, 2^-24 each, against a half step of 2^-9)."""
+    m = O.make(1, 4, 2, 300, 300, 64, 64, torch.bfloat16, seed=21)
+    got, want = run(cuda_lib, m, 2), O.gradients(**m)[0]
+    for n in got:
+        off = (got[n].cpu() != want[n].to(torch.bfloat16)).float().mean()
+        assert off < 0.02, (n, float(off))
+
+
+@pytest.mark.parametrize("shape", [(1, 8, 1, 600, 2000, 64, 64), (1, 4, 1, 40, 9000, 128, 128), (1, 16, 1, 700, 700, 192, 128),
+                                   (1, 2, 1, 16, 6000, 256, 256), (1, 3, 1, 30, 5000, 512, 512), (1, 6, 1, 900, 130, 72, 72)])
+@pytest.mark.parametrize("kind", ["full", "causal", "window"])
+def test_split_block_lists(cuda_lib, shape, kind):
+    """Few tiles with long block lists, which are cut into parts and joined; lists
+    of very different lengths (causal, window), so that some tiles have one part."""
+    if kind != "full" and shape[3] > shape[4]:
+        pytest.skip("causal needs L <= S")
+    kw = dict(full={}, causal=dict(causal=True), window=dict(causal=True, window=300))[kind]
+    for dtype in (torch.bfloat16, torch.float16):
+        check(cuda_lib, O.make(*shape, dtype, seed=22, **kw))
+
+
+def test_unknown_terms_are_refused(cuda_lib):
     m = O.make(1, 2, 2, 8, 8, 64, 64, torch.bfloat16)
-    with pytest.raises(cuda_lib.SdpaError) as ei:
-        run(cuda_lib, m, force_path=9)
-    assert ei.value.status == 1
+    for t in (-1, 3):
+        with pytest.raises(cuda_lib.SdpaError) as ei:
+            run(cuda_lib, m, t)
+        assert ei.value.status == 1
 
 
 def test_python_refusals_on_device(cuda_lib):

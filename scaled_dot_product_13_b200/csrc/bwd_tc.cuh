@@ -40,11 +40,18 @@
 // buffer: with ST = 1 it took 4300 cycles per 128 x 128 pairs of a key tile at
 // every head dim (E 1900 until the slower of an SM sub-partition's two warps is
 // through, then the two products and their hand-overs), against 2048 of tensor
-// work at head dim 128.  Two buffers of 64 columns let one warp group's
-// chain run under the other's.  Their cost is operand traffic: a 128 x 64 x 16
-// product with both operands in shared memory reads 6 KB (48 cycles) for 32
-// cycles of math.  So X, constant over a tile, is copied to TMEM where columns
-// are left and read from there (2 KB, 16 cycles).
+// work at head dim 128.  Two buffers let one warp group's chain run under the
+// other's.  Their cost is operand traffic: a 128 x 64 x 16 product with both
+// operands in shared memory reads 6 KB (48 cycles) for 32 cycles of math.  So X,
+// constant over a tile, is copied to TMEM where columns are left and read from
+// there (2 KB, 16 cycles).
+// What a block costs now, of the tensor work (cycles per block of 64, from CTA
+// times): head dim 128 key tiles 1370 of 1280, query tiles 1000 of 768; 256 dK and
+// dQ 2000 of 1792, dV 1270 of 1024.  At 128 and above the chip is at its power
+// limit under it (1000 W, 1.5 to 1.7 GHz of 1.96).  At 64 and 80 a block takes
+// about 1150 cycles of hand-overs whatever it computes (leaving out the
+// exponentials, or three quarters of the products, changed less than 5 %), so
+// those take blocks of 96 and 80 instead (6 % faster).
 //
 // TMEM (512 columns): ST stages of S and dP, out1, out2, X1, X2 where they fit:
 // BwdTcRoles below lists what each head-dim pair takes.  Head dims from 192/192
@@ -73,7 +80,7 @@ struct BwdTcRole {
   static constexpr int kBoxes1 = (D1 + 63) / 64, kBoxes2 = (D2 + 63) / 64;
   static constexpr int W1 = W_ ? W_ : D1, W2 = W_ ? W_ : D2;  // columns of out1, out2
   static constexpr bool PARTED = W_ != 0;
-  static constexpr int kBoxRows = BN == 32 ? 32 : 64;  // of the tensor maps of X and Y
+  static constexpr int kBoxRows = 64;  // of the tensor maps of X
   static constexpr uint32_t kX1Bytes = kBoxes1 * 128 * 128;
   static constexpr uint32_t kX2Bytes = OUT1 ? kBoxes2 * 128 * 128 : 0;  // dP only
   static constexpr uint32_t kY1Bytes = kBoxes1 * BN * 128;
@@ -125,8 +132,9 @@ struct BwdTcRole {
 };
 
 struct BwdTcMaps {
-  CUtensorMap q, k, v, dout;  // boxes of 64 rows (head dims 512: 32): X tiles, blocks
-  CUtensorMap qb, doutb;      // boxes of a key tile's blocks where those have other rows
+  CUtensorMap q, k, v, dout;  // boxes of 64 rows: X tiles
+  CUtensorMap qb, doutb;      // boxes of a key tile's blocks
+  CUtensorMap kb, vb;         // boxes of a query tile's blocks
   CUtensorMap dq, dk, dv;     // boxes of 128 rows
 };
 
@@ -683,11 +691,6 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         parts = in.query0;
         break;
       }
-      float nl[KEYS ? kH : 1];
-      if constexpr (KEYS) {
-#pragma unroll
-        for (int i = 0; i < kH; i += 4) *reinterpret_cast<float4 *>(nl + i) = *reinterpret_cast<const float4 *>(t_nlse + i);
-      }
       if (!(ok = wait(&s_full[st], ph))) break;
       // ---- phase E ----
       float w[kH];
@@ -695,24 +698,28 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       tmem_wait_ld();
       if constexpr (!OUT2) arrive(&p_full[st]);  // S_n is free
       const float2 c2 = make_float2(c, c);
+      // (all on the MUFU: with one pair in four on the FMA pipe's polynomial every
+      // head dim took 1 to 8 % longer)
 #pragma unroll
-      for (int i = 0; i < kH; i += 2) {
-        float2 t = fma2(make_float2(w[i], w[i + 1]), c2,
-                        KEYS ? make_float2(nl[KEYS ? i : 0], nl[KEYS ? i + 1 : 0]) : make_float2(x_nlse, x_nlse));
-        // (all on the MUFU: with one pair in four on the FMA pipe's polynomial every
-        // head dim took 1 to 8 % longer)
-        t.x = fast_exp2(t.x);
-        t.y = fast_exp2(t.y);
-        w[i] = t.x;
-        w[i + 1] = t.y;
+      for (int i = 0; i < kH; i += 4) {
+        float4 nl = make_float4(x_nlse, x_nlse, x_nlse, x_nlse);
+        if constexpr (KEYS) nl = *reinterpret_cast<const float4 *>(t_nlse + i);
+        const float2 t = fma2(make_float2(w[i], w[i + 1]), c2, make_float2(nl.x, nl.y));
+        const float2 u = fma2(make_float2(w[i + 2], w[i + 3]), c2, make_float2(nl.z, nl.w));
+        w[i] = fast_exp2(t.x);
+        w[i + 1] = fast_exp2(t.y);
+        w[i + 2] = fast_exp2(u.x);
+        w[i + 3] = fast_exp2(u.y);
       }
       if (in.masked) {
         // visible columns of this thread as bits
-        uint64_t seen = 0;
+        uint32_t seen[(kH + 31) / 32] = {};
         auto see = [&](int from, int to) {  // columns [from, to)
-          from = max(from, 0);
-          to = min(to, kH);
-          if (to > from) seen |= (~0ull >> (64 - (to - from))) << from;
+#pragma unroll
+          for (int j = 0; j < (kH + 31) / 32; ++j) {
+            const int lo = max(from - 32 * j, 0), hi = min(to - 32 * j, 32);
+            if (hi > lo) seen[j] |= (0xffffffffu >> (32 - (hi - lo))) << lo;
+          }
         };
         if constexpr (KEYS) {
           // one interval of queries per head that the block touches
@@ -726,7 +733,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         }
 #pragma unroll
         for (int e = 0; e < kH; ++e)
-          if (!((seen >> e) & 1)) w[e] = 0.f;
+          if (!((seen[e / 32] >> (e % 32)) & 1)) w[e] = 0.f;
       }
       if constexpr (OUT2) {
 #pragma unroll
@@ -747,33 +754,37 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       // ---- phase F ----
       if constexpr (OUT1) {
         if (!(ok = wait(&dp_full[st], ph))) break;
-        float d[kH];
-        tmem_ldn<kH>(t_dp, d);
-        tmem_wait_ld();
-        if (in.masked) {  // a masked pair's dP may be anything, also not a number
+        // columns at a time (two terms write past the columns they come from)
+        constexpr int kC = TWO ? kH : kH % 32 == 0 ? 32 : 16;
 #pragma unroll
-          for (int e = 0; e < kH; ++e)
-            if (w[e] == 0.f) d[e] = 0.f;
-        }
+        for (int j0 = 0; j0 < kH; j0 += kC) {
+          float d[kC];
+          tmem_ldn<kC>(t_dp + j0, d);
+          tmem_wait_ld();
+          if (in.masked) {  // a masked pair's dP may be anything, also not a number
 #pragma unroll
-        for (int j = 0; j < kH; j += 16) {
-          uint32_t pk[8], lo[8];
-#pragma unroll
-          for (int i = j; i < j + 16; i += 4) {
-            float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
-            if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + i);
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              float2 t = add2(make_float2(d[i + e], d[i + e + 1]),
-                              e == 0 ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w));
-              if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
-              t = mul2(t, make_float2(w[i + e], w[i + e + 1]));
-              pk[(i - j + e) / 2] = pack2<kBF16>(t.x, t.y);
-              if constexpr (TWO) lo[(i - j + e) / 2] = rest2<kBF16>(t.x, t.y, pk[(i - j + e) / 2]);
-            }
+            for (int e = 0; e < kC; ++e)
+              if (w[j0 + e] == 0.f) d[e] = 0.f;
           }
-          tmem_st_u8x(t_dp + j / 2, pk);
-          if constexpr (TWO) tmem_st_u8x(t_dp + kH / 2 + j / 2, lo);
+#pragma unroll
+          for (int j = 0; j < kC; j += 16) {
+            uint32_t pk[8], lo[8];
+#pragma unroll
+            for (int i = j; i < j + 16; i += 4) {
+              float4 nd = make_float4(x_ndelta, x_ndelta, x_ndelta, x_ndelta);
+              if constexpr (KEYS) nd = *reinterpret_cast<const float4 *>(t_ndelta + j0 + i);
+#pragma unroll
+              for (int e = i; e < i + 4; e += 2) {
+                float2 t = add2(make_float2(d[e], d[e + 1]), e == i ? make_float2(nd.x, nd.y) : make_float2(nd.z, nd.w));
+                if constexpr (!kBF16) t = mul2(t, make_float2(gain, gain));
+                t = mul2(t, make_float2(w[j0 + e], w[j0 + e + 1]));
+                pk[(e - j) / 2] = pack2<kBF16>(t.x, t.y);
+                if constexpr (TWO) lo[(e - j) / 2] = rest2<kBF16>(t.x, t.y, pk[(e - j) / 2]);
+              }
+            }
+            tmem_st_u8x(t_dp + (j0 + j) / 2, pk);
+            if constexpr (TWO) tmem_st_u8x(t_dp + kH / 2 + (j0 + j) / 2, lo);
+          }
         }
         tmem_wait_st();
         arrive(&ds_full[st]);
@@ -845,10 +856,10 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
 
 constexpr uint32_t bwd_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The kinds of tile of one head-dim pair, most work per block first: TMEM columns
+// The kinds of tile of one head-dim pair: TMEM columns
 //   pair      key tiles                          query tiles
-//   64/64     2 x 128 + 64 + 64  + X 32 + 32     2 x 128 + 64  + X 32 + 32
-//   80/80     2 x 128 + 80 + 80  + X 40 + 40     2 x 128 + 80  + X 40 + 40
+//   64/64     2 x 192 + 64 + 64                  2 x 192 + 64  + X 32 + 32
+//   80/80     2 x 160 + 80 + 80                  2 x 160 + 80  + X 40 + 40
 //   128/128   2 x 128 + 128 + 128                2 x 128 + 128 + X 64 + 64
 //   192/128   2 x  96 + 192 + 128                2 x 128 + 192 +   X2 64
 //   192/192   128 + 192 + X 96 + 96 (dK)         128 + 192 + X 96 + 96
@@ -859,20 +870,28 @@ constexpr uint32_t bwd_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 //             2 x  32 + 192 + X1 256 (dV)        192 gradient columns per CTA
 template <int DQK, int DV>
 struct BwdTcRoles;
-template <int D>
-struct BwdTcRolesBoth {
-  using Key = BwdTcRole<D, D, 64, 2, 4, 4, true, true, true, D <= 80, D <= 80>;
-  using Query = BwdTcRole<D, D, 64, 2, 4, 4, false, true, false, true, true>;
+template <>
+struct BwdTcRoles<64, 64> {
+  using Key = BwdTcRole<64, 64, 96, 2, 4, 4, true, true, true, false, false>;
+  using Query = BwdTcRole<64, 64, 96, 2, 4, 4, false, true, false, true, true>;
   using KeyV = void;
   // (more than half of an SM's, whatever the tiles need: a CTA takes all of TMEM)
   static constexpr uint32_t kSmem = bwd_max(120 * 1024, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
 };
 template <>
-struct BwdTcRoles<64, 64> : BwdTcRolesBoth<64> {};
+struct BwdTcRoles<80, 80> {
+  using Key = BwdTcRole<80, 80, 80, 2, 4, 4, true, true, true, false, false>;
+  using Query = BwdTcRole<80, 80, 80, 2, 4, 4, false, true, false, true, true>;
+  using KeyV = void;
+  static constexpr uint32_t kSmem = bwd_max(120 * 1024, bwd_max(Key::kSmemBytes, Query::kSmemBytes));
+};
 template <>
-struct BwdTcRoles<80, 80> : BwdTcRolesBoth<80> {};
-template <>
-struct BwdTcRoles<128, 128> : BwdTcRolesBoth<128> {};
+struct BwdTcRoles<128, 128> {
+  using Key = BwdTcRole<128, 128, 64, 2, 4, 4, true, true, true, false, false>;
+  using Query = BwdTcRole<128, 128, 64, 2, 4, 4, false, true, false, true, true>;
+  using KeyV = void;
+  static constexpr uint32_t kSmem = bwd_max(Key::kSmemBytes, Query::kSmemBytes);
+};
 template <>
 struct BwdTcRoles<192, 128> {
   using Key = BwdTcRole<192, 128, 48, 2, 4, 4, true, true, true, false, false>;
@@ -928,24 +947,23 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1)
   const int key_tiles = slabs * keys.tiles * keys.splits;
   const int key_ctas = key_tiles * bwd_col_parts<Key>(p.a.Dqk);
   const int row_ctas = slabs * rows.tiles * rows.splits * bwd_col_parts<Query>(p.a.Dqk);
-  const CUtensorMap *qb = Key::BN == Key::kBoxRows ? &tm.q : &tm.qb, *doutb = Key::BN == Key::kBoxRows ? &tm.dout : &tm.doutb;
   // the kind with the longest block lists first
   int id = blockIdx.x;
   if (rows_first) id = id < row_ctas ? (int)gridDim.x - row_ctas + id : id - row_ctas;
   if (id < key_ctas) {
-    bwd_tc_tile<kBF16, TWO, Key>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+    bwd_tc_tile<kBF16, TWO, Key>(p, &tm.k, &tm.v, &tm.qb, &tm.doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
     return;
   }
   id -= key_ctas;
   if constexpr (!std::is_void_v<KeyV>) {
     const int v_ctas = key_tiles * bwd_col_parts<KeyV>(p.a.Dv);
     if (id < v_ctas) {
-      bwd_tc_tile<kBF16, TWO, KeyV>(p, &tm.k, &tm.v, qb, doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
+      bwd_tc_tile<kBF16, TWO, KeyV>(p, &tm.k, &tm.v, &tm.qb, &tm.doutb, &tm.dk, &tm.dv, keys, id, smem_raw);
       return;
     }
     id -= v_ctas;
   }
-  bwd_tc_tile<kBF16, TWO, Query>(p, &tm.q, &tm.dout, &tm.k, &tm.v, &tm.dq, &tm.dq, rows, id, smem_raw);
+  bwd_tc_tile<kBF16, TWO, Query>(p, &tm.q, &tm.dout, &tm.kb, &tm.vb, &tm.dq, &tm.dq, rows, id, smem_raw);
 }
 
 // Sum of a tile's parts, where it has several, times the factor, rounded once: X rows of all

@@ -46,7 +46,9 @@ sdpa_status launch_bwd_f16(const BwdLaunch &ln, std::string *err);
 
 // Rows per block: query rows of a key tile's block, keys of
 // a query tile's.
-constexpr int bwd_tc_key_block(int dqk, int dv) { return dqk == 512 ? 32 : dqk == 192 && dv == 128 ? 48 : 64; }
-constexpr int bwd_tc_query_block(int dqk) { return dqk == 512 ? 32 : 64; }
+constexpr int bwd_tc_key_block(int dqk, int dv) {
+  return dqk == 64 ? 96 : dqk == 80 ? 80 : dqk == 512 ? 32 : dqk == 192 && dv == 128 ? 48 : 64;
+}
+constexpr int bwd_tc_query_block(int dqk, int dv) { return dqk == 64 ? 96 : dqk == 80 ? 80 : dqk == 512 ? 32 : 64; }
 
 }  // namespace sdpa

@@ -22,10 +22,8 @@ cudaError_t join(const BwdLaunch &ln, const BwdParams &p, const BwdTcSpan &span,
 template <bool kBF16, bool TWO, int DQK, int DV>
 sdpa_status run(const BwdLaunch &ln, std::string *err) {
   using Roles = BwdTcRoles<DQK, DV>;
-  constexpr int kBox = Roles::Query::kBoxRows;
-  static_assert(Roles::Key::BN == bwd_tc_key_block(DQK, DV) && Roles::Query::BN == bwd_tc_query_block(DQK),
+  static_assert(Roles::Key::BN == bwd_tc_key_block(DQK, DV) && Roles::Query::BN == bwd_tc_query_block(DQK, DV),
                 "the plan counts the kernel's blocks");
-  static_assert(Roles::Query::BN == kBox && Roles::Key::kBoxRows == kBox, "one map serves X tiles and key blocks");
   if constexpr (!std::is_void_v<typename Roles::KeyV>)
     static_assert(Roles::KeyV::BN == Roles::Key::BN, "both read the same boxes of Q and dO");
   auto kern = bwd_tc_kernel<kBF16, TWO, DQK, DV>;
@@ -52,19 +50,19 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
     const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
     return encode_tma(m, pb.dtype, 3, base, dims, strides, box, err);
   };
-  constexpr int BK = Roles::Key::BN;
+  constexpr int BK = Roles::Key::BN, BQ = Roles::Query::BN, BX = Roles::Key::kBoxRows;
   const int R = pl.rows, S = pb.S, Dqk = pb.Dqk, Dv = pb.Dv;
   BwdTcMaps tm;
-  if (!map(&tm.q, ln.q, Dqk, R, kBox) || !map(&tm.k, ln.k, Dqk, S, kBox) || !map(&tm.v, ln.v, Dv, S, kBox) ||
-      !map(&tm.dout, ln.dout, Dv, R, kBox) || !map(&tm.dq, ln.dq, Dqk, R, 128) ||
+  if (!map(&tm.q, ln.q, Dqk, R, BX) || !map(&tm.k, ln.k, Dqk, S, BX) || !map(&tm.v, ln.v, Dv, S, BX) ||
+      !map(&tm.dout, ln.dout, Dv, R, BX) || !map(&tm.dq, ln.dq, Dqk, R, 128) ||
       !map(&tm.dk, ln.dk, Dqk, S, 128) || !map(&tm.dv, ln.dv, Dv, S, 128))
     return SDPA_ERR_CUDA;
-  if (BK == kBox) {
-    tm.qb = tm.q;
-    tm.doutb = tm.dout;
-  } else if (!map(&tm.qb, ln.q, Dqk, R, BK) || !map(&tm.doutb, ln.dout, Dv, R, BK)) {
-    return SDPA_ERR_CUDA;
-  }
+  tm.qb = tm.q;
+  tm.doutb = tm.dout;
+  tm.kb = tm.k;
+  tm.vb = tm.v;
+  if (BK != BX && (!map(&tm.qb, ln.q, Dqk, R, BK) || !map(&tm.doutb, ln.dout, Dv, R, BK))) return SDPA_ERR_CUDA;
+  if (BQ != BX && (!map(&tm.kb, ln.k, Dqk, S, BQ) || !map(&tm.vb, ln.v, Dv, S, BQ))) return SDPA_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);

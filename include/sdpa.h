@@ -1,6 +1,7 @@
 /*
- * libsdpa: fused scaled-dot-product attention forward pass for NVIDIA B200
- * (sm_100a).
+ * libsdpa: fused scaled-dot-product attention for NVIDIA B200 (sm_100a): the
+ * forward pass, the backward pass, and the rotary positions on both sides of
+ * them.
  *
  *   O = softmax(scale * Q K^T + mask) V
  *
@@ -295,6 +296,9 @@ SDPA_API sdpa_status sdpa_forward_planned(const void *q, const void *k, const vo
  *   dq, dk, dv     gradients, shaped and typed like q, k, v; every element is
  *                  written (0 for keys that no row sees)
  *   the rest       as in the forward call; opt may be NULL
+ * out and lse may also be those of a merge over more keys than k and v hold (keys
+ * processed in chunks, or kept on several devices): each call then gives its
+ * own keys' dk and dv and their share of dq.
  * A row whose lse is -inf contributes nothing.  The sums run in a fixed order:
  * the same call gives the same bits.  P and dS enter their products as 16-bit
  * values, one or the sum of two (weight_terms; fp16: after scaling by powers of

@@ -1001,6 +1001,6 @@ const char *sdpa_status_string(sdpa_status s) {
 
 const char *sdpa_last_error_message(void) { return t_last_error.c_str(); }
 
-int sdpa_version(void) { return 100; }
+int sdpa_version(void) { return 200; }
 
 }  // extern "C"

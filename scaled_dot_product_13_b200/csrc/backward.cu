@@ -184,6 +184,12 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
              workspace == nullptr ? (size_t)0 : workspace_bytes);
     return refuse(SDPA_ERR_RESOURCES, buf);
   }
+  for (const Range &r : in)
+    if (!own_ws && r.n && extents_meet(workspace, pl.ws_bytes, r.p, r.n))
+      return refuse(SDPA_ERR_INVALID_ARG, "workspace must not overlap a tensor of the call");
+  for (const Range &r : to)
+    if (!own_ws && r.n && extents_meet(workspace, pl.ws_bytes, r.p, r.n))
+      return refuse(SDPA_ERR_INVALID_ARG, "workspace must not overlap a tensor of the call");
   ln.pb = pb;
   ln.q = q; ln.k = k; ln.v = v; ln.out = out; ln.dout = dout;
   ln.dq = dq; ln.dk = dk; ln.dv = dv;

@@ -10,16 +10,17 @@
 // slab sums the gradients of a shared KV head by itself, in a fixed order and
 // without atomics.
 //
-// Rounding: P and dS enter their products as 16-bit values, all sums and row
-// terms are fp32, each gradient is rounded once.  For fp16 both are
-// scaled by powers of two first (bf16 has fp32's exponents and needs none):
+// Rounding: P and dS enter their products as 16-bit values (one, or for small
+// problems the sum of two), all sums and row terms are fp32, each gradient is
+// rounded once.  For fp16 both are scaled by powers of two first (bf16 has fp32's exponents and needs none):
 //   - P by 2^14: P <= 1, and a weight of 2^-16 (one of 64K equal keys) would
 //     otherwise be a subnormal number;
-//   - dS by 2^14 gain: |dP - delta| <= 2 max||dO|| max||V|| + max|dlse| =: bound
-//     (Cauchy-Schwarz; O is a convex combination of V's rows), and gain is the
-//     power of two that takes bound into [1, 2).  So |dS| stays below 2^15 and
-//     cannot overflow, whatever the gradient's scale, and a loss scale is not
-//     needed to keep it from underflowing.
+//   - dS by 2^14 gain: |dP - delta| <= max||dO|| (max||V|| + max||O||) + max|dlse|
+//     =: bound (Cauchy-Schwarz), and gain is the power of two that takes bound
+//     into [1, 2).  So |dS| stays below 2^15 and cannot overflow, whatever the
+//     gradient's scale, and a loss scale is not needed to keep it from
+//     underflowing.  (O's own norm, although it is a mean of V's rows: out and
+//     lse may be those of more keys than the call's.)
 // The output factors take the powers of two back, exactly.
 #pragma once
 
@@ -31,8 +32,8 @@ struct BwdParams {
   AttnParams a;         // geometry, mask, scale_log2, watchdog (as in the forward kernels)
   const float *nlse;    // [B*Hkv][rpad] kPExp - lse log2(e); -inf: the row contributes nothing
   const float *ndelta;  // [B*Hkv][rpad] -delta
-  const unsigned int *norms;  // fp16: [B*Hkv][4] float bits of max||dO||, max||V||, max|dlse|
-  int rpad;             // R rounded up to 128
+  const unsigned int *norms;  // fp16: [B*Hkv][4] float bits of max||dO||, max||V||, max|dlse|, max||O||
+  int rpad;             // R rounded up so that every tile and block stays inside
   float scale;
   const void *q, *k, *v, *dout;
   void *dq, *dk, *dv;
@@ -51,7 +52,8 @@ __device__ __forceinline__ float bwd_gain(const BwdParams &p, int bh) {
   const float n_do = __uint_as_float(__ldg(p.norms + 4 * bh));
   const float n_v = __uint_as_float(__ldg(p.norms + 4 * bh + 1));
   const float n_l = __uint_as_float(__ldg(p.norms + 4 * bh + 2));
-  const float bound = 2.f * n_do * n_v + n_l;
+  const float n_o = __uint_as_float(__ldg(p.norms + 4 * bh + 3));
+  const float bound = n_do * (n_v + n_o) + n_l;
   if (!(bound > 0.f) || isinf(bound)) return 1.f;  // nothing to scale, or not finite anyway
   const int e = min(max(ilogbf(bound), -100), 100);
   return __int_as_float((127 - e) << 23);

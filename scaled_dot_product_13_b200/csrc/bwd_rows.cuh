@@ -3,7 +3,7 @@
 //   nlse   = kPExp - lse log2(e)        ndelta = dlse - rowsum(dO O)
 // over slabs padded to a multiple of 128 rows; padding rows and rows without a
 // visible key carry nlse = -inf, so that their P is 0 in every kernel without a
-// test.  For fp16 also the largest row norms of dO and V and the largest |dlse|
+// test.  For fp16 also the largest row norms of dO, O and V and the largest |dlse|
 // of each slab (an order-independent maximum over the bits of non-negative
 // floats), from which the gain on dS is taken.
 //
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
     const int r = (int)(prow - (long long)bh * p.rpad);
     const bool live = r < p.R;
     const long long row = (long long)bh * p.R + r;
-    float part[4] = {0.f, 0.f, 0.f, 0.f}, sq = 0.f;  // four short sums: less rounding than one
+    float part[4] = {0.f, 0.f, 0.f, 0.f}, sq = 0.f, sq_o = 0.f;  // four short sums: less rounding than one
     if (live) {
       const uint4 *o = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.out) + row * p.Dv);
       const uint4 *d = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dout) + row * p.Dv);
@@ -72,7 +72,10 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
         for (int i = 0; i < 4; ++i) {
           const float2 a = unpack2<kBF16>(ow[i]), b = unpack2<kBF16>(dw[i]);
           part[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, part[i]));
-          if constexpr (!kBF16) sq = fmaf(b.x, b.x, fmaf(b.y, b.y, sq));
+          if constexpr (!kBF16) {
+            sq = fmaf(b.x, b.x, fmaf(b.y, b.y, sq));
+            sq_o = fmaf(a.x, a.x, fmaf(a.y, a.y, sq_o));
+          }
         }
       }
     }
@@ -87,6 +90,7 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
     if constexpr (!kBF16) {
       block_max_to(p.norms + 4 * bh, sqrtf(sum8(sq)), tmp);
       block_max_to(p.norms + 4 * bh + 2, dl, tmp);
+      block_max_to(p.norms + 4 * bh + 3, sqrtf(sum8(sq_o)), tmp);
     }
   } else if constexpr (!kBF16) {
     const long long id = blockIdx.x - p.row_ctas;

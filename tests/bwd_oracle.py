@@ -81,7 +81,7 @@ def gradients(q, k, v, out, lse, dout, scale, causal=False, window=0, offset=Non
     es = (Dqk + 4) * E * abs(scale) * (q.abs() @ kT.abs()) + 2.0 ** -22 * (1 + fl + s.abs())
     ep = torch.where(seen, p * (uv + es) + (2.0 ** -39 if half else 0.0), 0.0)
     et = (Dv + 4) * E * (do.abs() @ vT.abs() + (do * out).abs().sum(-1, keepdim=True) + dl.abs()[..., None])
-    low = 2.0 ** -39 * (2 * do.norm(dim=-1).amax() * v.norm(dim=-1).amax() + dl.abs().amax()) if half else 0.0
+    low = 2.0 ** -39 * (do.norm(dim=-1).amax() * (v.norm(dim=-1).amax() + out.norm(dim=-1).amax()) + dl.abs().amax()) if half else 0.0
     eds = torch.where(seen, p * ((uv + es) * t.abs() + et) * (1 + 2 * u) + low, 0.0)
     sub = 2.0 ** -25 if half else 0.0
 

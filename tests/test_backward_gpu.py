@@ -174,8 +174,11 @@ def test_nothing_else_is_written(cuda_lib, terms, shape):
     for n in first:
         assert torch.equal(first[n], again[n]), n
     with pytest.raises(cuda_lib.SdpaError) as ei:
-        run(cuda_lib, m, terms, workspace=ws[pad:pad + need - 1][:need - 16], **outs)
+        run(cuda_lib, m, terms, workspace=ws[pad:pad + need - 16], **outs)
     assert ei.value.status == 3
+    with pytest.raises(cuda_lib.SdpaError) as ei:  # over an output
+        run(cuda_lib, m, terms, workspace=ws[pad:pad + need], **dict(outs, dq=ws[pad:pad + 2 * m["q"].numel()].view(m["q"].dtype).view(m["q"].shape)))
+    assert ei.value.status == 1 and "workspace" in ei.value.message
 
 
 @pytest.mark.parametrize("terms", TERMS)
@@ -246,6 +249,24 @@ def test_split_block_lists(cuda_lib, shape, kind):
     kw = dict(full={}, causal=dict(causal=True), window=dict(causal=True, window=300))[kind]
     for dtype in (torch.bfloat16, torch.float16):
         check(cuda_lib, O.make(*shape, dtype, seed=22, **kw))
+
+
+@pytest.mark.parametrize("terms", TERMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_keys_in_chunks(cuda_lib, terms, dtype):
+    """The gradients of a chunk of the keys, from the out and lse over all of them:
+    chunks whose values differ by a factor of 1000, in fp16 near its range."""
+    m = O.make(1, 4, 2, 120, 400, 64, 64, DT[dtype], seed=23)
+    m["v"][:, :, :150] *= 2.0 ** -10
+    m["v"][:, :, 150:] *= 2.0 ** 5
+    out, lse = O.forward(m["q"], m["k"], m["v"], m["scale"])
+    m["out"], m["lse"] = out.to(DT[dtype]), lse.float()
+    for lo, hi in ((0, 150), (150, 400)):
+        c = dict(m, k=m["k"][:, :, lo:hi].contiguous(), v=m["v"][:, :, lo:hi].contiguous())
+        got = run(cuda_lib, c, terms)
+        want, tol = O.gradients(**c, terms=terms)
+        for n in want:
+            assert ((got[n].double().cpu() - want[n]).abs() <= tol[n]).all(), (n, lo)
 
 
 def test_unknown_terms_are_refused(cuda_lib):

@@ -176,8 +176,10 @@ def test_nothing_else_is_written(cuda_lib, terms, shape):
     with pytest.raises(cuda_lib.SdpaError) as ei:
         run(cuda_lib, m, terms, workspace=ws[pad:pad + need - 16], **outs)
     assert ei.value.status == 3
+    big = torch.zeros(need + 2 * m["q"].numel(), dtype=torch.uint8, device="cuda")
+    over = big[:2 * m["q"].numel()].view(m["q"].dtype).view(m["q"].shape)
     with pytest.raises(cuda_lib.SdpaError) as ei:  # over an output
-        run(cuda_lib, m, terms, workspace=ws[pad:pad + need], **dict(outs, dq=ws[pad:pad + 2 * m["q"].numel()].view(m["q"].dtype).view(m["q"].shape)))
+        run(cuda_lib, m, terms, workspace=big[:need], **dict(outs, dq=over))
     assert ei.value.status == 1 and "workspace" in ei.value.message
 
 

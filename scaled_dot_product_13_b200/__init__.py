@@ -8,6 +8,8 @@ or a CUDA device is missing, calls raise.
 
     import scaled_dot_product_13_b200 as sdpa
     out = sdpa.forward(q, k, v, scale=None, causal=True, window_size=0)
+    dq, dk, dv = sdpa.backward(q, k, v, out, lse, dout, causal=True)   # lse from forward_ex
+    q, k = sdpa.rotary(sdpa.rotary_plan(128), q, k)
 
 q [B, Hq, L, Dqk], k [B, Hkv, S, Dqk], v [B, Hkv, S, Dv], contiguous CUDA
 tensors of one dtype (bfloat16 or float16).  Query head hq reads KV head
@@ -337,11 +339,17 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
     import torch
 
     lib = _LIB or load_library()
-    B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
-    dt = _dtype_code(q)
     dtype, device, f32 = q.dtype, q.device, torch.float32
+    qs, ks, vs = q.shape, k.shape, v.shape
+    if not (len(qs) == len(ks) == 4 and vs[:-1] == ks[:-1] and ks[0] == qs[0] and ks[3] == qs[3]
+            and q.is_cuda and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and k.dtype == dtype and v.dtype == dtype):
+        _shapes(q, k, v)  # names what is wrong
     if k.device != device or v.device != device:
         raise SdpaError(1, "k and v must be on q's device")
+    dt = _dtype_code(q)
+    B, Hq, L, Dqk = qs
+    Hkv, S, Dv = ks[1], ks[2], vs[3]
     rows = (B, Hq, L)
 
     def want(name, t, shape, kind):
@@ -384,8 +392,8 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
             ws_ptr = workspace.data_ptr()
     st = lib.sdpa_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), want("out", out, rows + (Dv,), dtype),
                            want("lse", lse, rows, f32), want("dout", dout, rows + (Dv,), dtype),
-                           want("dq", dq, q.shape, dtype), want("dk", dk, k.shape, dtype),
-                           want("dv", dv, v.shape, dtype), B, Hq, Hkv, L, S, Dqk, Dv,
+                           want("dq", dq, qs, dtype), want("dk", dk, ks, dtype),
+                           want("dv", dv, vs, dtype), B, Hq, Hkv, L, S, Dqk, Dv,
                            Dqk ** -0.5 if scale is None else scale, causal, window_size, dt, opt, ws_ptr, ws_bytes,
                            _call_stream(stream, device))
     if st:

@@ -251,7 +251,7 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t w) {
 template <int C0, int C1>
 __device__ __forceinline__ void bwd_x_to_tmem(const uint8_t *x, uint32_t taddr, int r) {
   static_assert(C0 % 4 == 0, "whole boxes");
-#pragma unroll 8
+#pragma unroll
   for (int c = C0; c < C1; ++c) {
     uint32_t v[8];
 #pragma unroll
@@ -755,7 +755,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       if constexpr (OUT1) {
         if (!(ok = wait(&dp_full[st], ph))) break;
         // columns at a time (two terms write past the columns they come from)
-        constexpr int kC = TWO ? kH : kH % 32 == 0 ? 32 : 16;
+        constexpr int kC = TWO ? kH : kH % 48 == 0 ? 48 : kH % 32 == 0 ? 32 : 16;
 #pragma unroll
         for (int j0 = 0; j0 < kH; j0 += kC) {
           float d[kC];
@@ -798,7 +798,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     const bool have_o = have && ok;
     const int nvalid = min(kBwdTcRows, xrows - x0);
     auto finish = [&](int col, int d, int first, int width, float factor, uint8_t *stage, float *out_part) {
-      const int chunks = min(width, d - first) / 16;
+      const int chunks = (Role::PARTED ? min(width, d - first) : width) / 16;
       for (int c16 = group * chunks / 2; c16 < (group + 1) * chunks / 2; ++c16) {
         float o[16];
         if (have_o) {

@@ -418,8 +418,10 @@ typedef struct {
  *       the dense [B][heads][L][head_dim] that sdpa_forward takes comes out, or
  *       the other way round for the gradient.  out may be x itself (same
  *       strides: in place); otherwise its extent must not meet x's.  Out
- *       strides must keep all elements apart.  The tensors of one call must not
- *       write what another of them reads or writes.
+ *       strides must keep all elements apart.  No tensor of a call may write
+ *       what another of them reads or writes: their extents must not meet, or
+ *       they are different heads of one array [B][L][heads][head_dim] or
+ *       [B][heads][L][head_dim] (equal batch and token strides).
  *   positions  device array of int32 (position_bits = 32) or int64 (64)
  *       positions, element [b * position_batch_stride + l]; NULL (bits 0):
  *       token l is at position l.  `offset` is added to every position.

@@ -215,6 +215,32 @@ bool apart(const sdpa_strides &s, int B, int heads, int L, int D) {
   return true;
 }
 
+// One view of a tensor: what a call reads or writes.
+struct View {
+  const void *p;
+  sdpa_strides s;
+  int heads;
+};
+
+// Whether two views share no element.  Extents that do not meet are enough; so
+// are head slices of one array, whose extents interleave: with equal batch (and
+// token) strides each view lies within one interval of every period, and the two
+// intervals must not meet.  Views that share a range in other ways count as
+// meeting.
+bool disjoint(const View &x, const View &y, int B, int L, int D) {
+  if (!extents_meet(x.p, 2 * extent(x.s, B, x.heads, L, D), y.p, 2 * extent(y.s, B, y.heads, L, D))) return true;
+  const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
+  if (bytes % 2 != 0 || x.s.batch != y.s.batch || x.s.token != y.s.token) return false;
+  auto slices = [&](long long period, int b, int l) {
+    if (period == 0) return false;
+    const long long nx = extent(x.s, b, x.heads, l, D), ny = extent(y.s, b, y.heads, l, D);
+    const long long at = ((bytes / 2) % period + period) % period;
+    return at >= nx && at + ny <= period;
+  };
+  // [B][heads][L][D], then [B][L][heads][D], whose batches are whole tokens apart
+  return slices(x.s.batch, 1, L) || (x.s.token != 0 && x.s.batch % x.s.token == 0 && slices(x.s.token, 1, 1));
+}
+
 }  // namespace
 }  // namespace sdpa
 
@@ -322,6 +348,7 @@ extern "C" SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan,
   };
   fit(R / 2);
   fit(D);
+  View reads[2], writes[2];
   for (int i = 0; i < count; ++i) {
     const sdpa_rotary_tensor &t = tensors[i];
     if (!t.x || !t.out) return bad("x and out must be non-NULL device pointers");
@@ -349,8 +376,13 @@ extern "C" SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan,
     p.t[i] = {static_cast<const uint16_t *>(t.x), static_cast<uint16_t *>(t.out),
               xs.batch, xs.head, xs.token, os.batch, os.head, os.token};
     p.heads[i] = t.heads;
+    reads[i] = {t.x, xs, t.heads};
+    writes[i] = {t.out, os, t.heads};
     if (p.heads[0] + p.heads[1] > 0xffff) return set_error(SDPA_ERR_UNSUPPORTED, "more than 65535 heads in one call");
   }
+  if (count == 2 && !(disjoint(writes[0], writes[1], B, L, D) && disjoint(writes[0], reads[1], B, L, D) &&
+                      disjoint(writes[1], reads[0], B, L, D)))
+    return bad("out must not overlap x or out of another tensor of the call");
   int sms;
   unsigned int *wd;
   uint64_t limit;

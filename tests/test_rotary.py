@@ -123,3 +123,41 @@ def test_python_checks():
         sdpa.rotary(plan, torch.zeros(2, 3, 64, dtype=torch.bfloat16))
     with pytest.raises(sdpa.SdpaError, match="rotary_plan"):
         sdpa.rotary(None, torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16))
+
+
+# Two tensors of one call: (x, out, heads, x strides, out strides) each, in elements of 2
+# bytes; B = 2, L = 4, D = 64.  FUSED: rows of 6 heads, [B][L][6][64]; HEADS: [B][6][L][64].
+FUSED, HEADS, DENSE = (1536, 64, 384), (1536, 256, 64), (512, 256, 64)
+X, Y, FAR, OUT = 0x100000, 0x200000, 0x300000, 0x400000
+
+
+@pytest.mark.parametrize("first,second,refused", [
+    ((X, OUT, 2, DENSE, DENSE), (Y, OUT, 2, DENSE, DENSE), True),                # the same output
+    ((X, OUT, 2, DENSE, DENSE), (Y, OUT + 2048 - 16, 2, DENSE, DENSE), True),     # outputs meet by 8 elements
+    ((X, OUT, 2, DENSE, DENSE), (Y, OUT + 2048, 2, DENSE, DENSE), False),         # one behind the other
+    ((X, Y, 2, DENSE, DENSE), (Y, OUT, 2, DENSE, DENSE), True),                   # writes the other's input
+    ((X, OUT, 2, DENSE, DENSE), (Y, X, 2, DENSE, DENSE), True),
+    ((X, OUT, 2, DENSE, DENSE), (X, FAR, 2, DENSE, DENSE), False),                # one input twice
+    ((X, X, 4, FUSED, FUSED), (X + 512, X + 512, 2, FUSED, FUSED), False),        # slices in place: heads 0-3, 4-5
+    ((X, X, 4, FUSED, FUSED), (X + 384, X + 384, 2, FUSED, FUSED), True),         # heads 0-3, 3-4
+    ((X, X, 4, FUSED, FUSED), (X + 640, X + 640, 2, FUSED, FUSED), True),         # heads 5-6: the next token's head 0
+    ((X, X, 4, HEADS, HEADS), (X + 2048, X + 2048, 2, HEADS, HEADS), False),
+    ((X, X, 4, HEADS, HEADS), (X + 1536, X + 1536, 2, HEADS, HEADS), True),
+    ((X, OUT, 2, DENSE, FUSED), (Y, OUT + 256, 4, (1024, 256, 64), FUSED), False),
+    ((X, OUT, 2, DENSE, FUSED), (Y, OUT + 256, 4, (1024, 256, 64), HEADS), True),  # layouts that cross
+])
+def test_tensors_of_a_call_kept_apart(first, second, refused):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up: an accepted call must find no device")
+    lib = sdpa.load_library()
+    plan = sdpa.rotary_plan(64)
+    t = (sdpa.RotaryTensor * 2)()
+    for i, (x, out, heads, xs, os_) in enumerate((first, second)):
+        t[i] = sdpa.RotaryTensor(x, out, heads, sdpa.Strides(*xs), sdpa.Strides(*os_))
+    st = lib.sdpa_rotary(ctypes.byref(plan), t, 2, 2, 4, None, 0, 0, 0, 0, 0, None)
+    msg = lib.sdpa_last_error_message().decode()
+    if refused:
+        assert st == 1 and "another tensor" in msg, (st, msg)
+    else:  # past the checks, stopped by the missing device
+        assert st not in (0, 1), (st, msg)

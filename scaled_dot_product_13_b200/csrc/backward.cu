@@ -28,7 +28,8 @@ constexpr long long kTwoTermPairs = 1 << 20;
 // loads and its share of the join cost more than the parallelism gives.
 constexpr int kMinBlocksPerPart = 4;
 // ... and a list is only split when it is this much longer than an SM's share:
-// at 1.3 (the causal 192/128 case, a ragged chunk) splitting cost 6 to 18 %.
+// limits of 1.0 to 1.2, which split lists of 1.3 shares, cost 2 to 6 % (the causal
+// 192/128 case) and 18 % (a ragged chunk), and gave nothing elsewhere.
 constexpr double kSplitOver = 1.5;
 
 sdpa_status make_bwd_plan(const Problem &pb, int sms, int weight_terms, BwdPlan *out) {

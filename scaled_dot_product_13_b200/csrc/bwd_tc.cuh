@@ -50,7 +50,7 @@
 // dQ 2000 of 1792, dV 1270 of 1024.  At 128 and above the chip is at its power
 // limit under it (1000 W, 1.5 to 1.7 GHz of 1.96).  At 64 and 80 a block takes
 // about 1150 cycles of hand-overs whatever it computes (leaving out the
-// exponentials, or three quarters of the products, changed less than 5 %), so
+// exponentials, or three quarters of one product, changed at most 6 %), so
 // those take blocks of 96 and 80 instead (6 % faster).
 //
 // TMEM (512 columns): ST stages of S and dP, out1, out2, X1, X2 where they fit:
@@ -698,8 +698,8 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       tmem_wait_ld();
       if constexpr (!OUT2) arrive(&p_full[st]);  // S_n is free
       const float2 c2 = make_float2(c, c);
-      // (all on the MUFU: with one pair in four on the FMA pipe's polynomial every
-      // head dim took 1 to 8 % longer)
+      // (all on the MUFU: with part of them on the FMA pipe's polynomial head dim 192
+      // took 6 to 8 % longer, 64 and 72 1 to 4 %, the others the same to 2 %)
 #pragma unroll
       for (int i = 0; i < kH; i += 4) {
         float4 nl = make_float4(x_nlse, x_nlse, x_nlse, x_nlse);

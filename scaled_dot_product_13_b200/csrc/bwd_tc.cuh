@@ -98,7 +98,7 @@ struct BwdTcRole {
   static constexpr uint32_t kY2Off = kY1Off + N1 * kY1Bytes;
   static constexpr uint32_t kTermOff = kY2Off + N2 * kY2Bytes;  // [NT][2][BN] row terms
   // row terms and block notes: behind Y1's slot where that is held until the block
-  // is done, else (released after S_n) ST more, so that block n's stay until P_n
+  // is done, else (released before P_n) ST more, so that block n's stay until P_n
   static constexpr int NT = OUT1 ? N1 : N1 + ST;
   static constexpr uint32_t kTermBytes = KEYS ? NT * 2 * BN * 4 : 0;
   static constexpr uint32_t kInfoOff = kTermOff + kTermBytes;  // [NT] BwdBlockInfo
@@ -121,7 +121,8 @@ struct BwdTcRole {
   static_assert(KEYS || (OUT1 && !OUT2), "query tiles give dQ");
   static_assert(ST == 1 || ST == 2, "");
   static_assert(kColsUsed <= 512, "TMEM columns");
-  // Y1_n is held until out1_n (without out1, until S_n), issued after S_{n+ST}
+  // Y1_n is held until out1_n, issued after S_{n+ST} (without out1, until S_n and
+  // until the softmax warps of block n have seen it)
   static_assert(N1 >= ST + 1 && N2 >= (OUT1 && OUT2 ? ST : 1), "ring slots");
   static_assert(!ALIAS || (XT1 && OUT1 != OUT2 && N1 >= kAliasSlots && kXFirst >= kBoxes1 - kXFirst), "");
   static_assert(W1 % 16 == 0 && W2 % 16 == 0 && (!PARTED || W1 % 64 == 0), "");
@@ -341,7 +342,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
     tma_prefetch_desc(tm_y2);
     for (int s = 0; s < N1; ++s) {
       mbar_init(&y1_full[s], 1);
-      mbar_init(&y1_empty[s], 1);
+      mbar_init(&y1_empty[s], 1 + (OUT1 ? 0 : kBwdTcSoftmaxWarps / ST));
     }
     for (int s = 0; s < N2; ++s) {
       mbar_init(&y2_full[s], 1);
@@ -690,6 +691,13 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
         blocks = in.row0;
         parts = in.query0;
         break;
+      }
+      // Without out1, Y1_n's slot waits for no weights of block n.  It must not be
+      // filled again before this warp has seen it full: two phases later the
+      // barrier's parity reads "not yet" again.
+      if constexpr (!OUT1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&y1_empty[slot]);
       }
       if (!(ok = wait(&s_full[st], ph))) break;
       // ---- phase E ----

@@ -45,14 +45,16 @@ __device__ __forceinline__ constexpr float bwd_p_exp() {
   return kBF16 ? 0.f : 14.f;
 }
 
-// Power of two on dP - delta for one KV head's slab (fp16 only).
+// Power of two on dP - delta for one KV head's slab (fp16 only).  (Plain loads: the
+// grid that writes the norms may still be running when a programmatic dependent
+// starts, so they are not read-only for its lifetime.)
 template <bool kBF16>
 __device__ __forceinline__ float bwd_gain(const BwdParams &p, int bh) {
   if constexpr (kBF16) return 1.f;
-  const float n_do = __uint_as_float(__ldg(p.norms + 4 * bh));
-  const float n_v = __uint_as_float(__ldg(p.norms + 4 * bh + 1));
-  const float n_l = __uint_as_float(__ldg(p.norms + 4 * bh + 2));
-  const float n_o = __uint_as_float(__ldg(p.norms + 4 * bh + 3));
+  const float n_do = __uint_as_float(p.norms[4 * bh]);
+  const float n_v = __uint_as_float(p.norms[4 * bh + 1]);
+  const float n_l = __uint_as_float(p.norms[4 * bh + 2]);
+  const float n_o = __uint_as_float(p.norms[4 * bh + 3]);
   const float bound = n_do * (n_v + n_o) + n_l;
   if (!(bound > 0.f) || isinf(bound)) return 1.f;  // nothing to scale, or not finite anyway
   const int e = min(max(ilogbf(bound), -100), 100);

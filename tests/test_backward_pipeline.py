@@ -99,3 +99,12 @@ def test_the_release_counts_the_softmax_warps():
     text = SOURCE.read_text()
     assert "mbar_init(&y1_empty[s], 1 + (OUT1 ? 0 : kBwdTcSoftmaxWarps / ST));" in text
     assert re.search(r"if constexpr \(!OUT1\) \{\s+__syncwarp\(\);\s+if \(lane == 0\) mbar_arrive\(&y1_empty\[slot\]\);", text)
+
+
+def test_no_read_only_loads_of_what_the_grid_before_writes():
+    """bwd_tc_kernel starts while bwd_rows_kernel may still write the row terms and
+    norms: a non-coherent load of them may be moved above the wait for it."""
+    for name in ("bwd_tc.cuh", "bwd_params.cuh"):
+        text = (SOURCE.parent / name).read_text()
+        kernel = text.split("bwd_join_kernel")[0]  # the join is an ordinary launch
+        assert "__ldg" not in kernel and ".nc" not in kernel, name

@@ -299,8 +299,13 @@ SDPA_API sdpa_status sdpa_forward_planned(const void *q, const void *k, const vo
  * out and lse may also be those of a merge over more keys than k and v hold (keys
  * processed in chunks, or kept on several devices): each call then gives its
  * own keys' dk and dv and their share of dq.
- * A row whose lse is -inf contributes nothing.  The sums run in a fixed order:
- * the same call gives the same bits.  P and dS enter their products as 16-bit
+ * A row whose lse is -inf (set so for the padding of a batch, say) takes no part:
+ * its dq is 0, and it has no share in dk, dv, dsinks or fp16's scaling, however
+ * large its q, out, dout and dlse are.  Its q and dout must be finite: they still meet
+ * weights of 0 in a product, so that an inf or NaN there reaches its KV head's dk or
+ * dv; its out and dlse may hold anything.
+ * The sums run in a fixed order: the same call gives the same bits.  P and dS enter
+ * their products as 16-bit
  * values, one or the sum of two (weight_terms; fp16: after scaling by powers of
  * two, so that small gradients need no loss scale); all sums are fp32.
  * Workspace: sdpa_backward_workspace_bytes(...) bytes, always above 0;

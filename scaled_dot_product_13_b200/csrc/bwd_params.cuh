@@ -30,7 +30,7 @@ namespace sdpa {
 
 struct BwdParams {
   AttnParams a;         // geometry, mask, scale_log2, watchdog (as in the forward kernels)
-  const float *nlse;    // [B*Hkv][rpad] kPExp - lse log2(e); -inf: the row contributes nothing
+  const float *nlse;    // [B*Hkv][rpad] kPExp - lse log2(e); -inf: the row takes no part
   const float *ndelta;  // [B*Hkv][rpad] -delta
   const unsigned int *norms;  // fp16: [B*Hkv][4] float bits of max||dO||, max||V||, max|dlse|, max||O||
   int rpad;             // R rounded up so that every tile and block stays inside

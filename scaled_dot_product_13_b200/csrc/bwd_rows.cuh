@@ -1,14 +1,17 @@
 // Row terms of the backward pass: one read of dO and O per query row.
 //
 //   nlse   = kPExp - lse log2(e)        ndelta = dlse - rowsum(dO O)
-// over slabs padded to a multiple of 128 rows; padding rows and rows without a
-// visible key carry nlse = -inf, so that their P is 0 in every kernel without a
-// test.  For fp16 also the largest row norms of dO, O and V and the largest |dlse|
+// over slabs padded to a multiple of 128 rows.  A row that takes no part (lse = -inf)
+// carries nlse = -inf and ndelta = 0 and has no share in the norms, whatever its dO,
+// O and dlse hold; padding rows, whose Q and dO are read as zeros, carry the lowest
+// finite nlse, so that their P is 0 without a test.  For fp16 also the largest row norms of dO, O and V and the largest |dlse|
 // of each slab (an order-independent maximum over the bits of non-negative
 // floats), from which the gain on dS is taken.
 //
 // Bound by memory: eight lanes share a row, 128 contiguous bytes per load.
 #pragma once
+
+#include <cfloat>
 
 #include "bwd_params.cuh"
 
@@ -80,14 +83,18 @@ __global__ void __launch_bounds__(kBwdRowsThreads) bwd_rows_kernel(const BwdRows
       }
     }
     const float dot = sum8((part[0] + part[1]) + (part[2] + part[3]));
+    const float lse = live ? p.lse[row] : 0.f;
+    const bool takes_part = live && lse != -INFINITY;
     float dl = 0.f;
-    if (live && p.dlse != nullptr) dl = p.dlse[row];
+    if (takes_part && p.dlse != nullptr) dl = p.dlse[row];
     if (sub == 0) {
-      const float lse = live ? p.lse[row] : -INFINITY;
-      p.nlse[prow] = lse == -INFINITY ? -INFINITY : bwd_p_exp<kBF16>() - lse * 1.4426950408889634f;
-      p.ndelta[prow] = live ? dl - dot : 0.f;
+      float nlse = bwd_p_exp<kBF16>() - lse * 1.4426950408889634f;
+      if (!live || nlse == -INFINITY) nlse = -FLT_MAX;  // (lse = +inf: exp(s - lse) = 0 as well)
+      p.nlse[prow] = lse == -INFINITY ? -INFINITY : nlse;
+      p.ndelta[prow] = takes_part ? dl - dot : 0.f;
     }
     if constexpr (!kBF16) {
+      if (!takes_part) sq = sq_o = 0.f;  // (the row's eight lanes agree)
       block_max_to(p.norms + 4 * bh, sqrtf(sum8(sq)), tmp);
       block_max_to(p.norms + 4 * bh + 2, dl, tmp);
       block_max_to(p.norms + 4 * bh + 3, sqrtf(sum8(sq_o)), tmp);

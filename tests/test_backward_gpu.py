@@ -123,6 +123,62 @@ def test_rows_without_keys(cuda_lib, terms, D):
 
 
 @pytest.mark.parametrize("terms", TERMS)
+@pytest.mark.parametrize("Dqk,Dv", [(64, 64), (72, 72), (128, 128), (192, 128), (192, 192), (256, 256), (320, 512), (16, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), None])
+def test_nothing_of_a_row_without_keys_reaches_a_gradient(cuda_lib, terms, Dqk, Dv, dtype, fill):
+    """Rows with lse = -inf (a padded batch): the largest finite numbers in their q and
+    dout, and anything in their out and dlse, give the same bits as zeros there, in all
+    gradients (the scores and dP overflow in bf16; fp16's scaling must not see them)."""
+    most = torch.finfo(DT[dtype]).max
+    for kw in (dict(causal=True, sinks=True, dlse=True), dict(dlse=True), dict(causal=True, window=50)):
+        m = O.make(2, 4, 2, 141, 170, Dqk, Dv, DT[dtype], seed=24, **kw)
+        dead = torch.zeros(2, 4, 141, dtype=torch.bool)
+        dead[0, 1, 5:40] = dead[0, 3, 140] = dead[0, 2, 0] = True
+        dead[1, :, 100:] = True  # the second sequence is shorter
+        m["lse"][dead] = -torch.inf
+        names = [n for n in ("q", "out", "dout", "dlse") if m[n] is not None]
+        for n in names:
+            m[n][dead] = 0
+        clean = check(cuda_lib, m, terms)
+        for n in names:
+            m[n][dead] = most if n in ("q", "dout") or fill is None else fill
+        m["q"][..., ::2] = torch.where(dead[..., None], -m["q"][..., ::2], m["q"][..., ::2])  # sums of both signs: inf - inf
+        got = run(cuda_lib, m, terms)
+        cuda_lib.device_status(clear=True)
+        for n in clean:
+            assert torch.equal(got[n], clean[n]), (n, kw)
+        assert (got["dq"][dead.cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_a_slab_of_rows_without_keys(cuda_lib, D):
+    """Every row of some query heads left out, and block lists cut into parts."""
+    for shape in ((1, 4, 2, 140, 140, D, D), (1, 4, 1, 40, 5000, D, D)):
+        m = O.make(*shape, torch.float16, seed=25)
+        m["lse"][:, :2] = -torch.inf
+        for n in ("q", "out", "dout"):
+            m[n][:, :2] = 0
+        clean = check(cuda_lib, m)
+        for n, x in (("q", 65504.0), ("out", float("nan")), ("dout", -65504.0)):
+            m[n][:, :2] = x
+        got = run(cuda_lib, m)
+        assert all(torch.equal(got[n], clean[n]) for n in clean)
+        assert (got["dq"][:, :2] == 0).all()
+
+
+@pytest.mark.parametrize("terms", TERMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_log_sum_exp_of_infinity(cuda_lib, terms, dtype):
+    """exp(s - inf) = 0 for every finite score: those rows' dq is 0, and the other
+    gradients those of the other rows."""
+    m = O.make(1, 4, 2, 100, 130, 64, 64, DT[dtype], seed=26)
+    m["lse"][0, 1, 3:70] = torch.inf
+    got = check(cuda_lib, m, terms)
+    assert (got["dq"][0, 1, 3:70] == 0).all()
+
+
+@pytest.mark.parametrize("terms", TERMS)
 def test_not_a_number_stays_in_its_slab(cuda_lib, terms):
     m = O.make(2, 4, 2, 100, 130, 64, 64, torch.float16, seed=15)
     clean = run(cuda_lib, m, terms)

@@ -72,14 +72,4 @@ __device__ __forceinline__ float bwd_ds_factor(const BwdParams &p, float gain) {
   return p.scale * bwd_dv_factor<kBF16>() / gain;
 }
 
-// Positions of packed rows [r0, r0 + n) of a slab (n >= 1 valid rows).
-__device__ __forceinline__ void packed_positions(const AttnParams &a, int r0, int n, int &pos_min,
-                                                 int &pos_max) {
-  const int i0 = r0 % a.L;
-  const int i1 = (r0 + n - 1) % a.L;
-  const bool wraps = n >= a.L || i1 < i0;  // over the end of a head's rows
-  pos_min = (wraps ? 0 : i0) + a.off;
-  pos_max = (wraps ? a.L - 1 : i1) + a.off;
-}
-
 }  // namespace sdpa

@@ -60,11 +60,11 @@
 
 #include <type_traits>
 
+#include "bwd_blocks.h"
 #include "bwd_params.cuh"
 
 namespace sdpa {
 
-constexpr int kBwdTcRows = 128;
 constexpr int kBwdTcSoftmaxWarps = 8;
 constexpr int kBwdTcThreads = (kBwdTcSoftmaxWarps + 2) * 32;
 
@@ -164,67 +164,6 @@ struct __align__(16) BwdBlockInfo {
   int masked;  // some pair of tile and block needs its own test
   int valid;   // 0 behind the last block
 };
-
-// The blocks of BN Y rows that a tile visits, in rising order.  Query tiles
-// see one range of keys.  Key tiles see, of each head's L packed rows, the same
-// range of queries [i_lo, i_hi); a block may span several heads.
-template <class Role>
-struct BwdBlocks {
-  int end;        // blocks end here
-  int L, R;
-  int lo, hi;     // packed rows of the current head that the tile sees
-  int base;       // first packed row of that head
-  bool all;       // every row is visible: nothing to skip
-
-  // Smallest visited block >= b (rising from call to call), or -1.  Leaves the
-  // first head with visible rows at or behind the block's first row as the
-  // current one.
-  __device__ __forceinline__ int at_or_after(int b) {
-    if (b >= end) return -1;
-    if constexpr (Role::KEYS) {
-      const int r0 = b * Role::BN;
-      while (r0 >= hi) {
-        lo += L;
-        hi += L;
-        base += L;
-        if (lo >= R) return -1;
-      }
-      if (!all && r0 + Role::BN <= lo) b = lo / Role::BN;
-    }
-    return b;
-  }
-
-  // Query index of packed row r0 (the first of the last returned block).
-  __device__ __forceinline__ int query(int r0) const {
-    return r0 >= base ? r0 - base : r0 - base + L;
-  }
-};
-
-template <class Role>
-__device__ __forceinline__ BwdBlocks<Role> bwd_blocks(const AttnParams &a, int x0, int &first) {
-  BwdBlocks<Role> w;
-  w.L = a.L;
-  w.R = a.R;
-  w.base = 0;
-  w.lo = 0;
-  w.hi = a.L;
-  first = 0;
-  if constexpr (Role::KEYS) {
-    const int key_max = min(x0 + kBwdTcRows, a.S) - 1;
-    if (a.causal) w.lo = min(max(x0 - a.off, 0), a.L);
-    if (a.window > 0) w.hi = (int)max(0LL, min((long long)a.L, (long long)key_max + a.window - a.off));
-    w.end = w.lo < w.hi ? (a.R + Role::BN - 1) / Role::BN : 0;
-  } else {
-    int pos_min, pos_max;
-    packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);
-    const int kend = a.causal ? min(a.S, pos_max + 1) : a.S;
-    const int kbeg = a.window > 0 ? max(0, pos_min - a.window + 1) : 0;
-    first = kbeg / Role::BN;
-    w.end = kend > kbeg ? (kend + Role::BN - 1) / Role::BN : first;
-  }
-  w.all = w.hi - w.lo == a.L;
-  return w;
-}
 
 // N consecutive TMEM columns of this thread's lane (N a multiple of 16).
 template <int N>
@@ -387,20 +326,17 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       const float *ndelta = p.ndelta + (long long)bh * p.rpad;
       // the block list of this CTA: `count` visited blocks from `begin`
       int begin, count = 0x7fffffff, parts = 1;
-      BwdBlocks<Role> walk = bwd_blocks<Role>(a, x0, begin);
+      BwdBlocks<KEYS, BN> walk = bwd_blocks<KEYS, BN>(a, x0);
       if (span.splits > 1) {
-        BwdBlocks<Role> w = walk;
-        int total = 0;
-        for (int b = w.at_or_after(begin); b >= 0; b = w.at_or_after(b + 1)) ++total;
+        int total;
+        begin = walk.seek(split * span.per, total);
         // (the last part takes what an estimate of `per` may have left)
         parts = min(span.splits, max(1, (total + span.per - 1) / span.per));
         count = total - split * span.per;
         if (split < span.splits - 1) count = min(span.per, count);
-        begin = walk.at_or_after(begin);
-        for (int s = 0; s < split * span.per && begin >= 0; ++s) begin = walk.at_or_after(begin + 1);
         if (split == 0) span.parts[bh * span.tiles + tile] = parts;
       } else {
-        begin = walk.at_or_after(begin);
+        begin = walk.at_or_after(walk.first);
       }
       int pos_min = 0, pos_max = 0;  // query tiles: the tile's positions
       if constexpr (!KEYS) packed_positions(a, x0, min(kBwdTcRows, a.R - x0), pos_min, pos_max);

@@ -422,11 +422,13 @@ typedef struct {
  *       that slices of a fused projection [B][L][heads][head_dim] go in and
  *       the dense [B][heads][L][head_dim] that sdpa_forward takes comes out, or
  *       the other way round for the gradient.  out may be x itself (same
- *       strides: in place); otherwise its extent must not meet x's.  Out
+ *       strides: in place); otherwise it must share no element with x.  Out
  *       strides must keep all elements apart.  No tensor of a call may write
- *       what another of them reads or writes: their extents must not meet, or
- *       they are different heads of one array [B][L][heads][head_dim] or
- *       [B][heads][L][head_dim] (equal batch and token strides).
+ *       what another of them reads or writes.  Interleaved views that share no
+ *       element are fine: heads of one array, whether [B][L][heads][head_dim],
+ *       [B][L][heads][3][head_dim], [L][B][heads][head_dim] or otherwise laid out
+ *       (views that interleave with strides in no relation to each other, which
+ *       would take a search to tell apart, are refused).
  *   positions  device array of int32 (position_bits = 32) or int64 (64)
  *       positions, element [b * position_batch_stride + l]; NULL (bits 0):
  *       token l is at position l.  `offset` is added to every position.

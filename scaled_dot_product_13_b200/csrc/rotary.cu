@@ -222,23 +222,61 @@ struct View {
   int heads;
 };
 
-// Whether two views share no element.  Extents that do not meet are enough; so
-// are head slices of one array, whose extents interleave: with equal batch (and
-// token) strides each view lies within one interval of every period, and the two
-// intervals must not meet.  Views that share a range in other ways count as
-// meeting.
+// Multiples lo .. hi of a stride.
+struct Term {
+  long long stride, lo, hi;
+};
+
+// Whether `at` plus one multiple of each of n terms (falling strides) can come within
+// less than D of 0.  What the terms behind the first can add bounds its multiples: two or
+// three of them where the strides nest, as in every dense layout and its slices.
+// Gives up, with true, after `steps`.
+bool reaches(const Term *t, int n, long long at, int D, int *steps) {
+  if (n == 0) return at > -D && at < D;
+  long long lo = 0, hi = 0;  // of the terms behind
+  for (int i = 1; i < n; ++i) {
+    lo += t[i].stride * t[i].lo;
+    hi += t[i].stride * t[i].hi;
+  }
+  // stride m in (-D - at - hi, D - at - lo)
+  const long long s = t[0].stride, from = 1 - D - at - hi, to = D - 1 - at - lo;
+  const long long first = std::max(t[0].lo, from >= 0 ? (from + s - 1) / s : -(-from / s));
+  const long long last = std::min(t[0].hi, to >= 0 ? to / s : -((-to + s - 1) / s));
+  for (long long m = first; m <= last; ++m) {
+    if (--*steps < 0) return true;
+    if (reaches(t + 1, n - 1, at + s * m, D, steps)) return true;
+  }
+  return false;
+}
+
+// Whether two views share no element: extents that do not meet, or else no pair of rows
+// whose distance is below D (rows of views whose strides are in no relation may take
+// too many steps: those count as sharing).
 bool disjoint(const View &x, const View &y, int B, int L, int D) {
   if (!extents_meet(x.p, 2 * extent(x.s, B, x.heads, L, D), y.p, 2 * extent(y.s, B, y.heads, L, D))) return true;
-  const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
-  if (bytes % 2 != 0 || x.s.batch != y.s.batch || x.s.token != y.s.token) return false;
-  auto slices = [&](long long period, int b, int l) {
-    if (period == 0) return false;
-    const long long nx = extent(x.s, b, x.heads, l, D), ny = extent(y.s, b, y.heads, l, D);
-    const long long at = ((bytes / 2) % period + period) % period;
-    return at >= nx && at + ny <= period;
+  Term t[6];
+  int n = 0;
+  auto add = [&](long long stride, long long lo, long long hi) {
+    if (stride == 0 || lo == hi) return;
+    int i = 0;
+    while (i < n && t[i].stride > stride) ++i;
+    if (i < n && t[i].stride == stride) {
+      t[i].lo += lo;
+      t[i].hi += hi;
+      return;
+    }
+    for (int j = n++; j > i; --j) t[j] = t[j - 1];
+    t[i] = {stride, lo, hi};
   };
-  // [B][heads][L][D], then [B][L][heads][D], whose batches are whole tokens apart
-  return slices(x.s.batch, 1, L) || (x.s.token != 0 && x.s.batch % x.s.token == 0 && slices(x.s.token, 1, 1));
+  add(y.s.batch, 0, B - 1);
+  add(y.s.head, 0, y.heads - 1);
+  add(y.s.token, 0, L - 1);
+  add(x.s.batch, 1 - B, 0);
+  add(x.s.head, 1 - x.heads, 0);
+  add(x.s.token, 1 - L, 0);
+  const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
+  int steps = 10000;
+  return !reaches(t, n, bytes / 2, D, &steps);  // (both are 2-byte aligned)
 }
 
 }  // namespace
@@ -368,7 +406,7 @@ extern "C" SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan,
     if (!apart(os, B, t.heads, L, D))
       return bad("out strides must keep the rows of head_dim elements apart");
     const bool same = t.x == t.out && xs.batch == os.batch && xs.head == os.head && xs.token == os.token;
-    if (!same && extents_meet(t.x, 2 * extent(xs, B, t.heads, L, D), t.out, 2 * extent(os, B, t.heads, L, D)))
+    if (!same && !disjoint({t.x, xs, t.heads}, {t.out, os, t.heads}, B, L, D))
       return bad("out must be x itself or not overlap it");
     fit(reinterpret_cast<uintptr_t>(t.x) / 2);
     fit(reinterpret_cast<uintptr_t>(t.out) / 2);

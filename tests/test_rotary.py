@@ -161,3 +161,94 @@ def test_tensors_of_a_call_kept_apart(first, second, refused):
         assert st == 1 and "another tensor" in msg, (st, msg)
     else:  # past the checks, stopped by the missing device
         assert st not in (0, 1), (st, msg)
+
+
+def _pair(first, second, B, L, D):
+    """(status, message) of a call with two tensors, each x, out, heads, x's and out's strides."""
+    lib = sdpa.load_library()
+    plan = sdpa.rotary_plan(D)
+    t = (sdpa.RotaryTensor * 2)()
+    for i, (x, out, heads, xs, os_) in enumerate((first, second)):
+        t[i] = sdpa.RotaryTensor(x, out, heads, sdpa.Strides(*xs), sdpa.Strides(*os_))
+    st = lib.sdpa_rotary(ctypes.byref(plan), t, 2, B, L, None, 0, 0, 0, 0, 0, None)
+    return st, lib.sdpa_last_error_message().decode()
+
+
+def _no_device():
+    if pytest.importorskip("torch").cuda.is_available():
+        pytest.skip("the addresses are made up: an accepted call must find no device")
+
+
+# batch, head and token strides of one head's element in an array of H heads
+LAYOUTS = {"BLH": lambda B, L, H, D: (L * H * D, D, H * D), "BHL": lambda B, L, H, D: (H * L * D, L * D, D),
+           "BLH3": lambda B, L, H, D: (L * H * 3 * D, 3 * D, H * 3 * D), "BL3H": lambda B, L, H, D: (L * 3 * H * D, D, 3 * H * D),
+           "LBH": lambda B, L, H, D: (H * D, D, B * H * D), "LBH3": lambda B, L, H, D: (H * 3 * D, 3 * D, B * H * 3 * D),
+           "HBL": lambda B, L, H, D: (L * D, B * L * D, D), "LHB": lambda B, L, H, D: (D, B * D, H * B * D)}
+STEP = {"BLH": lambda B, L, H, D: 2 * D, "BHL": lambda B, L, H, D: 2 * L * D, "BLH3": lambda B, L, H, D: D,
+        "BL3H": lambda B, L, H, D: H * D, "LBH": lambda B, L, H, D: 2 * D, "LBH3": lambda B, L, H, D: D,
+        "HBL": lambda B, L, H, D: 2 * B * L * D, "LHB": lambda B, L, H, D: 2 * B * D}  # from q to k
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("B,L", [(2, 4), (1, 7), (3, 1), (1, 1), (8, 4096)])
+def test_slices_of_one_projection_in_place(layout, B, L):
+    """q and k of one array, rotated in place in one call, in every order of its
+    dimensions: accepted; one element nearer to each other: refused."""
+    _no_device()
+    H, D = 2, 64
+    whole = 4 if layout in ("BLH", "BHL", "LBH", "HBL", "LHB") else H  # q's and k's heads next to each other
+    s = LAYOUTS[layout](B, L, whole, D)
+    k = X + 2 * STEP[layout](B, L, H, D)
+    st, msg = _pair((X, X, H, s, s), (k, k, H, s, s), B, L, D)
+    assert st not in (0, 1), (st, msg)
+    st, msg = _pair((X, X, H, s, s), (k - 2, k - 2, H, s, s), B, L, D)
+    assert st == 1 and "another tensor" in msg, (st, msg)
+    # the gradient into it, from dense tensors elsewhere
+    dense = LAYOUTS["BHL"](B, L, H, D)
+    st, msg = _pair((X + (1 << 40), X, H, dense, s), (X + (1 << 41), k, H, dense, s), B, L, D)
+    assert st not in (0, 1), (st, msg)
+
+
+def test_views_against_their_elements():
+    """Random views of small arrays: refused exactly when an element is shared."""
+    import random
+
+    _no_device()
+    rng, seen = random.Random(1), {True: 0, False: 0}
+    B, L, D = 2, 3, 4
+
+    def elements(p, h, s):
+        return {p // 2 + b * s[0] + i * s[1] + l * s[2] + d for b in range(B) for i in range(h) for l in range(L) for d in range(D)}
+
+    def view(h):
+        # nested in any order, with gaps, so that the elements of an output are apart
+        s, span = [0, 0, 0], D
+        for i in rng.sample(range(3), 3):
+            s[i] = span + rng.choice([0, 0, 1, D, 2 * D, 5 * D])
+            span = s[i] * ((B, h, L)[i] - 1) + span
+        return tuple(s)
+
+    for _ in range(4000):
+        h0, h1 = rng.randint(1, 3), rng.randint(1, 3)
+        s0 = view(h0)
+        s1 = s0 if rng.random() < 0.5 and h0 == h1 else view(h1)
+        at = X + 2 * rng.randint(-60, 60)
+        far0, far1 = X + (1 << 30), X + (1 << 31)
+        kind = rng.randint(0, 3)
+        if kind == 0:    # both in place
+            one, two = (X, X, h0, s0, s0), (at, at, h1, s1, s1)
+        elif kind == 1:  # outputs near each other
+            one, two = (far0, X, h0, s0, s0), (far1, at, h1, s1, s1)
+        elif kind == 2:  # one writes near what the other reads
+            one, two = (far0, X, h0, s0, s0), (at, far1, h1, s1, s1)
+        else:            # only read near each other: always fine
+            one, two = (X, far0, h0, s0, s0), (at, far1, h1, s1, s1)
+        shared = kind != 3 and bool(elements(X, h0, s0) & elements(at, h1, s1))
+        st, msg = _pair(one, two, B, L, D)
+        assert (st == 1) == shared and st != 0, (kind, at - X, h0, s0, h1, s1, st, msg)
+        seen[shared] += 1
+        # a tensor's own output near its input
+        if kind == 0 and (at != X or s0 != s1) and h0 == h1:
+            st, msg = _pair((X, at, h0, s0, s1), (far0, far1, h1, s1, s1), B, L, D)
+            assert (st == 1) == shared and st != 0, (at - X, h0, s0, s1, st, msg)
+    assert min(seen.values()) > 300, seen

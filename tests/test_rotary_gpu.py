@@ -221,3 +221,38 @@ def test_python_refusals_on_device(cuda_lib):
     assert ei.value.status == 2
     with pytest.raises(cuda_lib.SdpaError):
         cuda_lib.rotary(plan, torch.zeros(1, 1, 8, 128, dtype=torch.bfloat16, device="cuda")[..., ::2])
+
+
+@pytest.mark.parametrize("order", ["BLH", "BHL", "BLH3", "BL3H", "LBH", "LBH3", "HBL", "LHB"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_two_slices_of_one_array_in_every_layout(cuda_lib, order, interleaved):
+    """q and k as slices of one projection in any order of its dimensions, in place in
+    one call, and their gradient written into it: the same bits as from dense tensors,
+    and nothing else is touched."""
+    sizes = {"B": 3, "L": 29, "H": 5, "3": 3}
+    D, R = 72, 40
+    plan = cuda_lib.rotary_plan(D, rotary_dim=R, interleaved=interleaved)
+    x = made(tuple(sizes[c] for c in order) + (D,), torch.bfloat16, 13)
+
+    def parts(t):
+        """q (and k, v): three of the five heads each, or q, k, v of every head."""
+        if "3" in order:
+            three = [t.select(order.index("3"), i) for i in range(3)]
+            rest = order.replace("3", "")
+        else:
+            three = [t.narrow(order.index("H"), 0, 3), t.narrow(order.index("H"), 3, 1), t.narrow(order.index("H"), 4, 1)]
+            rest = order
+        return [p.permute(rest.index("B"), rest.index("H"), rest.index("L"), 3) for p in three]
+
+    q, k, v = parts(x)
+    want_q, want_k = cuda_lib.rotary(plan, q, k, offset=9)
+    check(want_q, q, (torch.arange(29) + 9).expand(3, 29), R, interleaved, False)
+    y = x.clone()
+    yq, yk, yv = parts(y)
+    cuda_lib.rotary(plan, yq, yk, offset=9, out_q=yq, out_k=yk)
+    assert torch.equal(yq, want_q) and torch.equal(yk, want_k) and torch.equal(yv, v)
+    z = torch.full_like(x, 7.0)
+    zq, zk, zv = parts(z)
+    cuda_lib.rotary(plan, want_q, want_k, offset=9, inverse=True, out_q=zq, out_k=zk)
+    back_q, back_k = cuda_lib.rotary(plan, want_q, want_k, offset=9, inverse=True)
+    assert torch.equal(zq, back_q) and torch.equal(zk, back_k) and (zv == 7.0).all()

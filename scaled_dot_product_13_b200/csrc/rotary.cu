@@ -403,6 +403,9 @@ extern "C" SDPA_API sdpa_status sdpa_rotary(const sdpa_rotary_plan *plan,
     const sdpa_strides xs = used(t.x_strides), os = used(t.out_strides);
     for (long long st : {xs.batch, xs.head, xs.token, os.batch, os.head, os.token})
       if (st < 0 || st > (1LL << 40)) return bad("strides must lie in [0, 2^40] (got %.0f)", (double)st);
+    for (const sdpa_strides &st : {xs, os})  // (later sums of them stay in 64 bits)
+      if ((__int128)(B - 1) * st.batch + (__int128)(t.heads - 1) * st.head + (__int128)(L - 1) * st.token > (1LL << 48))
+        return bad("strides must keep a tensor within 2^48 elements");
     if (!apart(os, B, t.heads, L, D))
       return bad("out strides must keep the rows of head_dim elements apart");
     const bool same = t.x == t.out && xs.batch == os.batch && xs.head == os.head && xs.token == os.token;

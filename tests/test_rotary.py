@@ -252,3 +252,10 @@ def test_views_against_their_elements():
             st, msg = _pair((X, at, h0, s0, s1), (far0, far1, h1, s1, s1), B, L, D)
             assert (st == 1) == shared and st != 0, (at - X, h0, s0, s1, st, msg)
     assert min(seen.values()) > 300, seen
+
+
+def test_strides_past_the_address_space():
+    st, msg = _call(xs=(1 << 40, 256, 64), B=1 << 20, L=4)
+    assert st == 1 and "2^48" in msg, (st, msg)
+    st, msg = _call(os_=(1 << 20, 64, 1 << 40), B=2, L=1 << 29)
+    assert st == 1 and "2^48" in msg, (st, msg)

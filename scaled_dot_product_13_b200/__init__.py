@@ -14,6 +14,10 @@ or a CUDA device is missing, calls raise.
 q [B, Hq, L, Dqk], k [B, Hkv, S, Dqk], v [B, Hkv, S, Dv], contiguous CUDA
 tensors of one dtype (bfloat16 or float16).  Query head hq reads KV head
 hq // (Hq // Hkv); query i sits at key position i + S - L.
+
+``stream`` (a torch stream or a handle; default the current one): where a call
+runs.  Tensors that a call makes are that stream's, as under
+``torch.cuda.stream(stream)``; what it is given must be ready there.
 """
 from __future__ import annotations
 
@@ -192,12 +196,28 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _out_like(q, L, Dv, out):
+def _allocating_on(stream, device):
+    """The context in which a call on ``stream`` makes its tensors: the allocator
+    hands out memory that earlier work of the stream asked for is done with, and
+    only of that stream."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _out_like(q, L, Dv, out, stream):
     import torch
 
     B, Hq = q.shape[0], q.shape[1]
     if out is None:
-        return torch.empty((B, Hq, L, Dv), dtype=q.dtype, device=q.device)
+        with _allocating_on(stream, q.device):
+            return torch.empty((B, Hq, L, Dv), dtype=q.dtype, device=q.device)
     if tuple(out.shape) != (B, Hq, L, Dv) or out.dtype != q.dtype or not out.is_contiguous():
         raise SdpaError(1, "out must be a contiguous [B, Hq, L, Dv] tensor of q's dtype")
     return out
@@ -209,7 +229,7 @@ def forward(q, k, v, scale: float | None = None, causal: bool = False, window_si
     lib = load_library()
     B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
     sc = float(Dqk ** -0.5 if scale is None else scale)
-    out = _out_like(q, L, Dv, out)
+    out = _out_like(q, L, Dv, out, stream)
     _check(lib.sdpa_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, Hq,
                             Hkv, L, S, Dqk, Dv, sc, int(bool(causal)), int(window_size),
                             _dtype_code(q), _stream(stream)))
@@ -226,7 +246,7 @@ def forward_noalloc(q, k, v, scale: float | None = None, causal: bool = False,
     lib = load_library()
     B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
     sc = float(Dqk ** -0.5 if scale is None else scale)
-    out = _out_like(q, L, Dv, out)
+    out = _out_like(q, L, Dv, out, stream)
     _check(lib.sdpa_forward_noalloc(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B,
                                     Hq, Hkv, L, S, Dqk, Dv, sc, int(bool(causal)),
                                     int(window_size), _dtype_code(q), _stream(stream)))
@@ -245,7 +265,7 @@ def forward_ex(q, k, v, scale: float | None = None, causal: bool = False, window
     lib = load_library()
     B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
     sc = float(Dqk ** -0.5 if scale is None else scale)
-    out = _out_like(q, L, Dv, out)
+    out = _out_like(q, L, Dv, out, stream)
     opt = Options()
     if q_offset is not None:
         opt.has_q_offset, opt.q_offset = 1, int(q_offset)
@@ -276,7 +296,7 @@ def forward_ws(q, k, v, workspace, scale: float | None = None, causal: bool = Fa
     lib = load_library()
     B, Hq, Hkv, L, S, Dqk, Dv = _shapes(q, k, v)
     sc = float(Dqk ** -0.5 if scale is None else scale)
-    out = _out_like(q, L, Dv, out)
+    out = _out_like(q, L, Dv, out, stream)
     ws_ptr = 0 if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.sdpa_forward_planned(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -377,9 +397,13 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
             return backward(q, k, v, out, lse, dout, scale, causal, window_size, q_offset, sinks, dlse, dq, dk, dv,
                             dsinks, stream, workspace, weight_terms)
     # (q, k and v are contiguous)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    if stream is not None:
+        with _allocating_on(stream, device):
+            dq, dk, dv = (torch.empty_like(x) if d is None else d for x, d in ((q, dq), (k, dk), (v, dv)))
+    else:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
     ws_ptr = ws_bytes = 0
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
@@ -454,9 +478,9 @@ def rotary(plan: RotaryPlan, q, k=None, positions=None, offset: int = 0, inverse
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return rotary(plan, q, k, positions, offset, inverse, out_q, out_k, stream)
-    out_q, fields = _rotary_tensor("q", q, out_q, plan.head_dim, B, L, dtype, device)
+    out_q, fields = _rotary_tensor("q", q, out_q, plan.head_dim, B, L, dtype, device, stream)
     if k is not None:
-        out_k, more = _rotary_tensor("k", k, out_k, plan.head_dim, B, L, dtype, device)
+        out_k, more = _rotary_tensor("k", k, out_k, plan.head_dim, B, L, dtype, device, stream)
         fields += more
     pos_ptr, bits, pos_stride = None, 0, 0
     if positions is not None:
@@ -481,7 +505,7 @@ def rotary(plan: RotaryPlan, q, k=None, positions=None, offset: int = 0, inverse
 _ROTARY_TENSOR = "QQi4xqqqqqq"
 
 
-def _rotary_tensor(name, x, out, D, B, L, dtype, device):
+def _rotary_tensor(name, x, out, D, B, L, dtype, device, stream):
     """The checked output of one tensor, and the fields of its sdpa_rotary_tensor."""
     import torch
 
@@ -494,7 +518,11 @@ def _rotary_tensor(name, x, out, D, B, L, dtype, device):
     if xd != 1:
         raise SdpaError(1, f"{name}'s last dim must be contiguous")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        if stream is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            with _allocating_on(stream, device):
+                out = torch.empty(shape, dtype=dtype, device=device)
     elif out.shape != shape or out.dtype != dtype or out.device != device or out.stride(3) != 1:
         raise SdpaError(1, f"out_{name} must have {name}'s shape, dtype and device, its last dim contiguous")
     ob, oh, ot, _ = out.stride()

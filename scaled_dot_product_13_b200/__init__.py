@@ -450,8 +450,11 @@ def _call_stream(stream, device):
     """The handle of ``stream``, by default the current stream of ``device``."""
     import torch
 
-    if stream is None:  # (without the Stream object that current_stream makes: 0.2 us, not 2.4)
-        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        # without the Stream object that current_stream makes: 0.2 us, not 2.4; but the
+        # function is torch's own and may be gone from another version
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -259,3 +259,12 @@ def test_strides_past_the_address_space():
     assert st == 1 and "2^48" in msg, (st, msg)
     st, msg = _call(os_=(1 << 20, 64, 1 << 40), B=2, L=1 << 29)
     assert st == 1 and "2^48" in msg, (st, msg)
+
+
+def test_current_stream_without_torchs_private_function(monkeypatch):
+    torch = pytest.importorskip("torch")
+    device = torch.device("cuda", 1)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: type("S", (), {"cuda_stream": 77 if d == device else 0}))
+    assert sdpa._call_stream(None, device) == 77
+    assert sdpa._call_stream(5, device) == 5

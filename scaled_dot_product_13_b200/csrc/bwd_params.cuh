@@ -56,7 +56,7 @@ __device__ __forceinline__ float bwd_gain(const BwdParams &p, int bh) {
   const float n_l = __uint_as_float(p.norms[4 * bh + 2]);
   const float n_o = __uint_as_float(p.norms[4 * bh + 3]);
   const float bound = n_do * (n_v + n_o) + n_l;
-  if (!(bound > 0.f) || isinf(bound)) return 1.f;  // nothing to scale, or not finite anyway
+  if (!(bound > 0.f)) return 1.f;  // nothing to scale
   const int e = min(max(ilogbf(bound), -100), 100);
   return __int_as_float((127 - e) << 23);
 }

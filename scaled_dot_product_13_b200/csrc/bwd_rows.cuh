@@ -36,9 +36,11 @@ __device__ __forceinline__ float sum8(float x) {
   return x;
 }
 
-// Block maximum of non-negative values (NaN wins: its bits are above inf's).
+// Block maximum of the sizes of finite values.  (A row that holds an inf or NaN has
+// no finite dS to scale; counted, it would take the scale from the other rows'.)
 __device__ __forceinline__ void block_max_to(unsigned int *cell, float x, unsigned int *tmp) {
   unsigned int m = __float_as_uint(x) & 0x7fffffffu;
+  if (m >= 0x7f800000u) m = 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = m;

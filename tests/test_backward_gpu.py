@@ -192,6 +192,30 @@ def test_not_a_number_stays_in_its_slab(cuda_lib, terms):
 
 
 @pytest.mark.parametrize("terms", TERMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name,x", [("dout", float("nan")), ("dout", float("inf")), ("out", float("inf")), ("dlse", float("nan")), ("q", float("inf"))])
+def test_a_row_that_is_not_finite_keeps_to_its_own_dq(cuda_lib, terms, dtype, name, x):
+    """Its KV head's dk and dv are lost, but the other rows' dq are what they are without
+    it: fp16's scaling, taken from the sizes of all rows, must not go with it (values at
+    which an unscaled dS overflows)."""
+    m = O.make(1, 4, 2, 150, 200, 64, 64, DT[dtype], seed=27, causal=True, dlse=True, dout_scale=64.0)
+    if name == "dlse":
+        m[name][0, 1, 77] = x
+    else:
+        m[name][0, 1, 77, 5] = x
+    got = run(cuda_lib, m, terms)
+    cuda_lib.device_status(clear=True)
+    m[name][0, 1, 77] = 0
+    want, tol = O.gradients(**m, terms=terms)
+    keep = torch.ones(1, 4, 150, dtype=torch.bool)
+    keep[0, 1, 77] = False
+    err = (got["dq"].double().cpu() - want["dq"]).abs()[keep]
+    assert (err <= tol["dq"][keep]).all(), float((err - tol["dq"][keep]).max())
+    for n in ("dk", "dv"):  # the other KV head's
+        assert ((got[n][:, 1].double().cpu() - want[n][:, 1]).abs() <= tol[n][:, 1]).all()
+
+
+@pytest.mark.parametrize("terms", TERMS)
 def test_future_values_that_are_not_numbers(cuda_lib, terms):
     """Keys that the causal mask hides from every row of a whole block do not
     reach it: their blocks are skipped."""

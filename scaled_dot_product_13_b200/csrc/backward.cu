@@ -209,8 +209,7 @@ extern "C" SDPA_API sdpa_status sdpa_backward(
   ln.stream = cs;
 
   std::string err;
-  st = launch_bwd_rows(ln, &err);
-  if (st == SDPA_OK) st = dtype == SDPA_BF16 ? launch_bwd_bf16(ln, &err) : launch_bwd_f16(ln, &err);
+  st = dtype == SDPA_BF16 ? launch_bwd_bf16(ln, &err) : launch_bwd_f16(ln, &err);
   if (st == SDPA_OK && dsinks) {
     bwd_sinks_kernel<<<Hq, kBwdSinksThreads, 0, cs>>>(sinks, lse, ln.ndelta, dsinks, B, Hq, Hkv, L, pl.rpad);
     cudaError_t e = cudaGetLastError();
@@ -243,7 +242,7 @@ sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err) {
   p.row_ctas = slabs * p.rpad / kBwdRowsPerCta;
   p.v_ctas = bf16 ? 0 : (pb.S + kBwdRowsPerCta - 1) / kBwdRowsPerCta;
   const long long ctas = p.row_ctas + slabs * p.v_ctas;
-  if (ctas > 0x7fffffffLL) {
+  if (ctas > 0x7fffffffLL) {  // (the first launch of a call: nothing is enqueued yet)
     *err = "problem needs more than 2^31 CTAs for its row terms";
     return SDPA_ERR_UNSUPPORTED;
   }

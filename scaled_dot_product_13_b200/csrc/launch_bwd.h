@@ -40,7 +40,8 @@ struct BwdLaunch {
 // Kernel parameters.
 void fill_bwd_params(const BwdLaunch &ln, BwdParams *p);
 
-sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err);
+sdpa_status launch_bwd_rows(const BwdLaunch &ln, std::string *err);  // row terms
+// ... and all products
 sdpa_status launch_bwd_bf16(const BwdLaunch &ln, std::string *err);
 sdpa_status launch_bwd_f16(const BwdLaunch &ln, std::string *err);
 

@@ -64,6 +64,9 @@ sdpa_status run(const BwdLaunch &ln, std::string *err) {
   if (BK != BX && (!map(&tm.qb, ln.q, Dqk, R, BK) || !map(&tm.doutb, ln.dout, Dv, R, BK))) return SDPA_ERR_CUDA;
   if (BQ != BX && (!map(&tm.kb, ln.k, Dqk, S, BQ) || !map(&tm.vb, ln.v, Dv, S, BQ))) return SDPA_ERR_CUDA;
 
+  // (behind every check that may still refuse the call)
+  st = launch_bwd_rows(ln, err);
+  if (st != SDPA_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kBwdTcThreads);

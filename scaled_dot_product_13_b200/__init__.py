@@ -15,6 +15,10 @@ q [B, Hq, L, Dqk], k [B, Hkv, S, Dqk], v [B, Hkv, S, Dv], contiguous CUDA
 tensors of one dtype (bfloat16 or float16).  Query head hq reads KV head
 hq // (Hq // Hkv); query i sits at key position i + S - L.
 
+No call records anything for autograd: results carry no graph, also where inputs
+require grad (use ``backward`` and ``rotary(..., inverse=True)`` in a
+``torch.autograd.Function``).
+
 ``stream`` (a torch stream or a handle; default the current one): where a call
 runs.  Tensors that a call makes are that stream's, as under
 ``torch.cuda.stream(stream)``; what it is given must be ready there.
@@ -350,8 +354,12 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
     in that call.  ``dlse``: gradient [B, Hq, L] (float32) of lse, where it was
     used.  ``dsinks``: float32 [Hq] that receives the gradient of ``sinks``.
     ``dq`` / ``dk`` / ``dv``: contiguous tensors to write (new ones when None).
-    ``weight_terms``: 16-bit terms that P and dS enter their products as, 1 or 2
-    (0: 2 for small problems, where it costs no time).
+    ``weight_terms``: 16-bit terms that P and dS enter their products as, 1 or 2: the
+    gradients' error is up to 1.45 times that of exact weights with 1, not noticeably
+    above it with 2, which takes up to 1.4 times as long (0: 2 up to B Hq L S = 2^20,
+    where it costs 0 to 30 %).
+    Rows with lse = -inf take no part (their q and dout must be finite).  Out and lse
+    merged over chunks of keys: add up the calls' dq, but take dsinks from one.
     ``workspace``: at least ``backward_workspace_bytes`` bytes on the device,
     not used by other work until the call's kernels are done.  None: from
     torch's caching allocator on the current stream, or, with ``stream`` given,

@@ -624,7 +624,7 @@ namespace {
 // Recently encoded tensor maps of this host thread.  A descriptor depends only
 // on its arguments (no device state), so an eager loop of calls on the same
 // tensors reuses it instead of encoding it again; a few entries cover the
-// last calls (a backward call has up to nine).
+// last calls (a backward call has seven to eleven).
 struct TmaCacheEntry {
   bool used;
   int dt;  // CUtensorMapDataType

@@ -17,19 +17,24 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 sdpa_status refuse(sdpa_status st, const char *msg) { return set_error(st, msg); }
 
 // Up to this many pairs of row and key, P and dS enter their products as two
-// 16-bit terms.  With few pairs the rounding of single weights does not average out
-// (up to 1.8 times the error of exact weights at a handful of rows, 1.45 at most
-// above 2^20 pairs), and a call is bound by latency: 12.3 us with two terms against
-// 10.3 to 11.9 with one at 2^20 pairs of head dim 64, on the device; at 2^22 it is
-// 57 against 52 at head dim 256, and 15 % at 2^25.
+// 16-bit terms unless the caller says otherwise.  What it steadies is the error of the
+// results as a whole: one term's is 1.41 times that of exact weights on average at any
+// size, up to 1.8 times where the whole call has a handful of rows, 1.45 at most above
+// 2^20 pairs.  (A single row's error is no smaller for the other rows of a call.)  What
+// it costs below the limit, on the device, one term against two: 8.3 and 8.3 us at 16 x
+// 16, 9.3 and 12.2 at 4 heads of 128 x 128, 10.3 and 12.4 at 8 of 362 x 362 (head dim
+// 64), 26.5 and 26.7 at 4 of 512 x 512 (256), 158 and 167 at 16 rows over 60000 keys;
+// above it 50 and 54 at 2^22 pairs of head dim 256, 62 and 86 at 2^25 of 64.
 constexpr long long kTwoTermPairs = 1 << 20;
 
 // Blocks each part of a split tile keeps at least: below that its operand
 // loads and its share of the join cost more than the parallelism gives.
 constexpr int kMinBlocksPerPart = 4;
-// ... and a list is only split when it is this much longer than an SM's share:
-// limits of 1.0 to 1.2, which split lists of 1.3 shares, cost 2 to 6 % (the causal
-// 192/128 case) and 18 % (a ragged chunk), and gave nothing elsewhere.
+// ... and lists are only split when the longest is this much longer than an SM's
+// share; then every list of more than `per` blocks is cut.  Limits of 1.0 to 1.2 cut the
+// causal 192/128 case, whose longest list is 1.3 shares, at half of that, and most of
+// its lists with it: 2 to 6 % slower (a ragged chunk 18 %; no gain elsewhere).  Cutting
+// the few longest alone was not tried.
 constexpr double kSplitOver = 1.5;
 
 sdpa_status make_bwd_plan(const Problem &pb, int sms, int weight_terms, BwdPlan *out) {
@@ -54,8 +59,9 @@ sdpa_status make_bwd_plan(const Problem &pb, int sms, int weight_terms, BwdPlan 
   // Split a tile's block list where one tile would outlast the whole grid's
   // work spread over the SMs (few tiles with long lists: few query rows over
   // many keys, one KV head under many rows, the first keys of a causal call).
-  // Work in pairs of row and key that the mask leaves, times 4 products in a
-  // key tile, 3 in a query tile.
+  // Work in pairs of row and key, times 4 products in a key tile, 3 in a query tile:
+  // an SM's share by the pairs that the mask leaves, a list by its whole tiles, so that
+  // a few rows, which fill little of a tile, are cut into more parts than they need.
   const int g = pb.Hq / pb.Hkv;
   const double first = pb.causal ? std::min<double>(pb.S, pb.q_offset + 1.0) : pb.S;
   const double last = pb.causal ? std::min<double>(pb.S, (double)pb.q_offset + pb.L) : pb.S;

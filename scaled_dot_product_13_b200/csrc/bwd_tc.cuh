@@ -237,8 +237,8 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xh_full + 1);
   constexpr int kProducerWarp = kBwdTcSoftmaxWarps, kMmaWarp = kBwdTcSoftmaxWarps + 1;
   constexpr bool XT = Role::XT1 || Role::XT2;
-  // (through a shuffle, so that the compiler knows the roles' branches to be
-  // warp-uniform and keeps the MMA operands in uniform registers)
+  // (through a shuffle, which tells the compiler that the roles' branches are
+  // warp-uniform)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // --- work item.  Key tiles: tile fastest (a slab's query blocks stay in L2

@@ -392,10 +392,9 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 }
 
 // The same MMAs and commit, executed by a whole converged warp of which the
-// lane with `leader` set issues (elect_leader, once per warp role).  Control flow
-// and operands then stay warp-uniform, and an MMA costs its issuer 20 to 60 cycles;
-// issued from inside a one-lane branch it costs 70 to 95 (every operand is moved
-// to the uniform registers again), which bounds the rate of MMAs with N <= 128.
+// lane with `leader` set issues (elect_leader, once per warp role).  Measured: an MMA
+// costs its issuer 20 to 60 cycles this way, and 70 to 95 from inside a one-lane
+// branch, which bounds the rate of MMAs with N <= 128.
 __device__ __forceinline__ uint32_t elect_leader() {
   uint32_t r;
   asm volatile(

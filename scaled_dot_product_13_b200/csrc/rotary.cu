@@ -12,8 +12,8 @@
 // requested before the angles are computed.
 // (2) Frequencies are 64-bit fixed-point turns per position: position * turns
 // wraps modulo one turn by itself, exactly; the top 32 bits are the angle in
-// 2^-32 turns, converted to half-turns in fp32 (relative error 2^-24) for
-// sincospif.  A float product position * w would be off by 2^-24 * t radians,
+// 2^-32 turns, converted to half-turns in fp32 (relative error 2^-24, at most 2^-26 of
+// a turn) for sincospif.  A float product position * w would be off by 2^-24 * t radians,
 // i.e. 0.008 at position 131072 in the first pair.
 #include <cuda_runtime.h>
 
@@ -312,8 +312,8 @@ extern "C" SDPA_API sdpa_status sdpa_rotary_init(const sdpa_rotary_config *c,
   if (!std::isfinite(c->magnitude) || c->magnitude < 0)
     return bad("magnitude must be finite and not negative (got %g)", c->magnitude);
 
-  // In extended precision: an error of 2^-64 relative in a frequency stays
-  // below 2^-32 turns at every 32-bit position.
+  // In extended precision: a frequency, below a sixth of a turn, is off by about 2^-64,
+  // its angle by less than 2^-32 of a turn at positions up to 2^30.
   const long double kTwoPi = 6.283185307179586476925286766559L;
   long double b = base;
   const long double f = c->scaling == SDPA_ROPE_PLAIN ? 1.0L : (long double)c->factor;

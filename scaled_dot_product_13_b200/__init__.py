@@ -21,7 +21,8 @@ require grad (use ``backward`` and ``rotary(..., inverse=True)`` in a
 
 ``stream`` (a torch stream or a handle; default the current one): where a call
 runs.  Tensors that a call makes are that stream's, as under
-``torch.cuda.stream(stream)``; what it is given must be ready there.
+``torch.cuda.stream(stream)``, and may be used on the stream that is current at the
+call once that waits for it; what a call is given must be ready on ``stream``.
 """
 from __future__ import annotations
 
@@ -200,28 +201,29 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _allocating_on(stream, device):
-    """The context in which a call on ``stream`` makes its tensors: the allocator
-    hands out memory that earlier work of the stream asked for is done with, and
-    only of that stream."""
-    import contextlib
-
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream`` (None: the current one) to write.  Its
+    memory is that stream's, so that nothing pending on another stream still uses it;
+    and as the current stream is where it is likely read, it is not given to a later
+    call before the work that is on the current stream when it is released is done."""
     import torch
 
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if here != stream:
+        t.record_stream(here)
+    return t
 
 
 def _out_like(q, L, Dv, out, stream):
-    import torch
-
     B, Hq = q.shape[0], q.shape[1]
     if out is None:
-        with _allocating_on(stream, q.device):
-            return torch.empty((B, Hq, L, Dv), dtype=q.dtype, device=q.device)
+        return _empty((B, Hq, L, Dv), q.dtype, q.device, stream)
     if tuple(out.shape) != (B, Hq, L, Dv) or out.dtype != q.dtype or not out.is_contiguous():
         raise SdpaError(1, "out must be a contiguous [B, Hq, L, Dv] tensor of q's dtype")
     return out
@@ -404,14 +406,14 @@ def backward(q, k, v, out, lse, dout, scale: float | None = None, causal: bool =
         with torch.cuda.device(device):
             return backward(q, k, v, out, lse, dout, scale, causal, window_size, q_offset, sinks, dlse, dq, dk, dv,
                             dsinks, stream, workspace, weight_terms)
-    # (q, k and v are contiguous)
-    if stream is not None:
-        with _allocating_on(stream, device):
-            dq, dk, dv = (torch.empty_like(x) if d is None else d for x, d in ((q, dq), (k, dk), (v, dv)))
-    else:
+    if stream is None:  # (q, k and v are contiguous)
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
+    else:
+        dq = _empty(qs, dtype, device, stream) if dq is None else dq
+        dk = _empty(ks, dtype, device, stream) if dk is None else dk
+        dv = _empty(vs, dtype, device, stream) if dv is None else dv
     ws_ptr = ws_bytes = 0
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
@@ -518,8 +520,6 @@ _ROTARY_TENSOR = "QQi4xqqqqqq"
 
 def _rotary_tensor(name, x, out, D, B, L, dtype, device, stream):
     """The checked output of one tensor, and the fields of its sdpa_rotary_tensor."""
-    import torch
-
     shape = x.shape
     if len(shape) != 4 or shape[3] != D:
         raise SdpaError(1, f"{name} must be [B, H, L, {D}] (got {tuple(shape)})")
@@ -529,11 +529,7 @@ def _rotary_tensor(name, x, out, D, B, L, dtype, device, stream):
     if xd != 1:
         raise SdpaError(1, f"{name}'s last dim must be contiguous")
     if out is None:
-        if stream is None:
-            out = torch.empty(shape, dtype=dtype, device=device)
-        else:
-            with _allocating_on(stream, device):
-                out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype, device, stream)
     elif out.shape != shape or out.dtype != dtype or out.device != device or out.stride(3) != 1:
         raise SdpaError(1, f"out_{name} must have {name}'s shape, dtype and device, its last dim contiguous")
     ob, oh, ot, _ = out.stride()

@@ -49,6 +49,28 @@ def test_outputs_belong_to_the_stream_of_the_call(cuda_lib, name, kind):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("name", ["backward", "rotary", "forward", "forward_ex", "forward_noalloc", "forward_ws"])
+def test_outputs_that_the_current_stream_still_reads(cuda_lib, name):
+    """A result of another stream, read by the current one and released: the next call
+    does not get its memory before that read is done."""
+    call = _calls(cuda_lib)[name]
+    want = [t.clone() for t in call()]
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    read = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(side):  # what comes next on that stream takes released memory
+        late = [torch.full((B, H, L, D), 7, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del late
+    assert all(torch.equal(a, b) for a, b in zip(read, want))
+
+
 def test_the_default_stream_by_its_handle(cuda_lib):
     for name, call in _calls(cuda_lib).items():
         want = call()
@@ -65,6 +87,23 @@ def test_captured_on_the_stream_that_is_passed(cuda_lib):
             got = call(stream=torch.cuda.current_stream())
         for t in got:
             t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_captured_on_a_stream_of_its_own(cuda_lib):
+    """A branch of a captured graph: the side stream joins the capture and is joined."""
+    for name, call in _calls(cuda_lib).items():
+        want = [t.clone() for t in call()]
+        g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g):
+            side.wait_stream(torch.cuda.current_stream())
+            got = call(stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name

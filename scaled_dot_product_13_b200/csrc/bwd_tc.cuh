@@ -638,7 +638,7 @@ __device__ __forceinline__ void bwd_tc_tile(const BwdParams &p, const CUtensorMa
       // Rows that take no part, among this warp's columns, as bits: masked, since their
       // scores and dP may have overflowed.  (Their Q and dO still enter the second
       // products, with weights of 0.  Zeros in their place, written here or by a warp of
-      // its own, took head dims 192/128 5 to 11 % longer, with such rows or without.)
+      // its own, took head dims 192/128 5 to 12 % longer, with such rows or without.)
       constexpr int kWords = (kH + 31) / 32;
       uint32_t gone[kWords] = {};
       bool dead = false;

@@ -4,9 +4,9 @@
 // over slabs padded to a multiple of 128 rows.  A row that takes no part (lse = -inf)
 // carries nlse = -inf and ndelta = 0 and has no share in the norms, whatever its dO,
 // O and dlse hold; padding rows, whose Q and dO are read as zeros, carry the lowest
-// finite nlse, so that their P is 0 without a test.  For fp16 also the largest row norms of dO, O and V and the largest |dlse|
-// of each slab (an order-independent maximum over the bits of non-negative
-// floats), from which the gain on dS is taken.
+// finite nlse, so that their P is 0 without a test.  For fp16 also the largest finite
+// row norms of dO, O and V and the largest |dlse| of each slab (an order-independent
+// maximum over the bits of non-negative floats), from which the gain on dS is taken.
 //
 // Bound by memory: eight lanes share a row, 128 contiguous bytes per load.
 #pragma once
